@@ -161,6 +161,33 @@ pa_status pa_pool_enable_prefix_cache(pa_pool* pool);
 pa_status pa_seq_alloc_prompt(pa_pool* pool, const int32_t* tokens, int32_t num_tokens, int32_t* table,
                               int32_t table_cap, int32_t* num_cached_tokens);
 
+/* pa_reserve_slots_with_updates for chunks: sequence s reserves counts[s] >= 0
+ * tokens (as that many pa_seq_reserve_slot calls on row s of `tables`, one
+ * sequence after another).  slots_out (room for the sum of counts) receives the
+ * slots packed in sequence order; at most one copy-on-write pair per sequence
+ * goes to pairs_out ([S][2] room); updates_out (or NULL) receives the table
+ * entries written, (row0 + s, column, block id), room for the sum over s of
+ * ceil(counts[s] / block_size) + 1 triples.  All or nothing.  Errors as for
+ * pa_seq_reserve_slot, and PA_ERR_INVALID for a negative count. */
+pa_status pa_reserve_chunks(pa_pool* pool, int32_t* tables, int32_t table_cap, int32_t* lens,
+                            const int32_t* counts, int32_t num_seqs, int32_t row0, int64_t* slots_out,
+                            int32_t* pairs_out, int32_t* num_pairs_out, int32_t* updates_out,
+                            int32_t* num_updates_out);
+
+/* Compaction: the live blocks are renamed so that they are blocks 0..n-1, n
+ * their number.  The k-th live block at or behind n (by id) takes the id of the
+ * k-th free block before n; moves_out ([num_blocks / 2][2] room) receives these
+ * (old id, new id) pairs in increasing order of both, *num_moves_out their
+ * count.  The caller must run the moves on every layer's cache
+ * (pa_move_blocks) before the new ids are used on the device.
+ * Reference counts and prefix-cache entries move along, the old id takes the
+ * new id's place in the free list, and every entry of `tables`
+ * ([num_rows][table_cap], host; may be NULL with num_rows 0) that names a moved
+ * block is rewritten.  Tables that are not passed must be rewritten by the
+ * caller.  Errors: PA_ERR_INVALID (bad argument; nothing is changed). */
+pa_status pa_pool_compact(pa_pool* pool, int32_t* tables, int32_t table_cap, int32_t num_rows,
+                          int32_t* moves_out, int32_t* num_moves_out);
+
 /* Number of blocks currently findable by key. */
 pa_status pa_pool_cached_blocks(const pa_pool* pool, int32_t* out);
 
@@ -206,6 +233,104 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* pairs, int
 pa_status pa_update_block_tables(int32_t* block_tables, int32_t num_rows, int32_t table_stride,
                                  const int32_t* updates, int32_t num_updates, int32_t* context_lens,
                                  const int32_t* new_lens, int32_t num_lens, void* stream);
+
+/* Rotary positions and append of a chunk of new tokens, in one launch.  For
+ * token t and rotary pair i < rotary_dim / 2 the angle is
+ *   positions[pair_axis[i]][t] * inv_freq[i]   (radians, worked out in 64 bits)
+ * and the two elements (a, b) of that pair of every query and key head become
+ * (a cos - b sin, b cos + a sin), computed in float32 and rounded once.  Pair i
+ * is the elements (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved is
+ * non-zero; elements from rotary_dim on are unchanged.  The turned queries go
+ * to q_out, the turned keys and the unchanged values to slot slot_mapping[t]
+ * as in pa_append_kv (a negative slot writes no key or value; a slot outside
+ * the cache is skipped and sets device error 3).
+ *
+ *   q, k_new, v_new  device rows of [Hq][D] (q) and [Hkv][D], one per token,
+ *                    *_stride elements apart (multiples of 16 bytes), so that
+ *                    slices of one projection can be passed
+ *   positions        device int32 [num_axes][num_tokens] (any sign)
+ *   inv_freq         device float32 [rotary_dim / 2]
+ *   pair_axis        device int32 [rotary_dim / 2], each in [0, num_axes)
+ *                    (another value takes axis 0 and sets device error 6), or
+ *                    NULL: axis 0 for every pair
+ *   q_out            device [T][Hq][D]; may be q when its rows are contiguous,
+ *                    and overlaps no other argument
+ * Slots must be distinct.  head_dim up to 512 whose bytes are a multiple of 32;
+ * rotary_dim even, at most head_dim.  Errors: PA_ERR_INVALID,
+ * PA_ERR_UNSUPPORTED, PA_ERR_CUDA. */
+pa_status pa_rope_append(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride,
+                         const void* v_new, int64_t v_stride, const int32_t* positions, int32_t num_axes,
+                         const float* inv_freq, const int32_t* pair_axis, int32_t rotary_dim,
+                         int32_t interleaved, const int64_t* slot_mapping, int32_t num_tokens, void* q_out,
+                         void* k_cache, void* v_cache, int32_t num_blocks, int32_t block_size,
+                         int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, pa_dtype dtype,
+                         void* stream);
+
+/* Block moves of a compaction, for all layers in one launch (one per 64
+ * layers): in each of num_layers caches (host arrays of device pointers, each
+ * [num_blocks][block_size][Hkv][D]), K and V block moves[i][1] become bit
+ * copies of block moves[i][0]; and every entry of block_tables (device int32
+ * [num_rows][num_cols], rows table_stride apart; NULL with num_rows 0) that
+ * names a source is rewritten to its destination.
+ *   moves  device int32 [num_moves][2], 8-byte aligned, sources strictly
+ *          increasing (as pa_pool_compact lists them; otherwise device error 7
+ *          is set and entries may be left unwritten); destinations distinct,
+ *          none of them a source, the caches distinct.
+ * Ids outside [0, num_blocks) are skipped and set device error 4.  Errors:
+ * PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_CUDA. */
+pa_status pa_move_blocks(void* const* k_caches, void* const* v_caches, int32_t num_layers,
+                         const int32_t* moves, int32_t num_moves, int32_t num_blocks, int32_t block_size,
+                         int32_t num_kv_heads, int32_t head_dim, int32_t* block_tables, int32_t num_rows,
+                         int32_t num_cols, int32_t table_stride, pa_dtype dtype, void* stream);
+
+/* Bytes of device workspace pa_prefill_attention takes for these sizes, of any
+ * dtype: the work list, and the partial results of contexts that are split over
+ * the GPU (their number is bounded by the SM count, not by the context).  0 for
+ * invalid sizes. */
+size_t pa_prefill_workspace_size(int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
+                                 int32_t num_kv_heads, int32_t head_dim, int32_t max_blocks_per_seq,
+                                 int32_t block_size);
+
+/* Attention of a chunk of tokens per sequence over the paged cache.  The rows
+ * of sequence s are the tokens q_starts[s] <= t < q_starts[s + 1] of the packed
+ * array q; with n their number, i = t - q_starts[s], kv = h / (Hq / Hkv):
+ *   out[t][h] = softmax_j(q[t][h] . K_s[j][kv] * scale) V_s[j][kv],  j < lim,
+ *   lim = context_lens[s] - n + i + 1   causal != 0: the chunk is the end of
+ *                                       its context, which already holds the
+ *                                       chunk's own keys and values (append
+ *                                       first), and a token sees no later one;
+ *   lim = context_lens[s]               causal == 0: every token sees the
+ *                                       whole context (cross attention to an
+ *                                       encoder's states kept in the cache).
+ * A row with lim <= 0 is zero.  K_s, V_s as for pa_decode_attention; a chunk of
+ * one token with causal != 0 is that call's row.  Scores, softmax statistics
+ * and output are accumulated in float32; for f16 and bf16 caches the weights
+ * are rounded to that type for the product with V.  Results do not depend on
+ * scheduling: equal calls give equal bits.
+ *
+ *   q, out        device [T][Hq][D]; rows of out from q_starts[S] on (and
+ *                 before q_starts[0]) are not written
+ *   q_starts      device int32 [S + 1], 0 <= non-decreasing <= num_tokens
+ *   block_tables  device int32 [S][max_blocks_per_seq]; entries that cover
+ *                 tokens < context_lens[s] must be valid block ids
+ *   context_lens  device int32 [S], each in [0, max_blocks_per_seq*block_size]
+ *   workspace     device buffer of pa_prefill_workspace_size() bytes, 32-byte
+ *                 aligned, owned by the caller; calls that share one must not
+ *                 overlap on the GPU.
+ * Cache slots at or behind a context's end may hold anything.  Values of
+ * *later* tokens of the same chunk must be finite: they are multiplied by a
+ * weight of zero.  Lengths or starts out of range are clamped and set device
+ * error 2; block ids outside the pool set device error 1.
+ * Supported: head_dim 64 or 128; Hq/Hkv in {1,2,4,8}; block_size a multiple of
+ * 16, or 8; f32/f16/bf16.  Errors: PA_ERR_INVALID, PA_ERR_UNSUPPORTED,
+ * PA_ERR_CUDA. */
+pa_status pa_prefill_attention(const void* q, const void* k_cache, const void* v_cache, int32_t num_blocks,
+                               const int32_t* block_tables, int32_t max_blocks_per_seq,
+                               const int32_t* context_lens, const int32_t* q_starts, int32_t num_tokens,
+                               int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                               int32_t head_dim, int32_t block_size, float scale, int32_t causal,
+                               void* workspace, size_t workspace_bytes, void* out, pa_dtype dtype,
+                               void* stream);
 
 /* Bytes of device workspace pa_decode_attention takes for these sizes: 256
  * bytes for the work-unit counter, a planned work-unit list of 16 bytes per
@@ -429,7 +554,9 @@ pa_status pa_engine_synchronize(pa_engine* engine);
  * device: 0 = none; 1 = block id outside the pool in a table; 2 =
  * context length beyond the table; 3 = append slot outside the cache; 4 =
  * copy pair id outside the pool; 5 = a pipeline wait of a kernel ran out of
- * time (that kernel returned early and its output is undefined).
+ * time (that kernel returned early and its output is undefined); 6 = axis of
+ * a rotary pair outside the positions; 7 = sources of a move list not in
+ * increasing order.
  * Synchronous: waits for the device. */
 pa_status pa_device_error(int32_t* code_out, int32_t reset);
 

@@ -23,9 +23,10 @@ Modules:
 ``pool``       host block pool: FIFO free list, refcounts, fork and the
                per-token slot reservation with copy-on-write.
 ``cache_ops``  the two cache-maintenance operations: write of new K/V into
-               slots, and whole-block copy.
+               slots, and whole-block copy; rotary positions.
 ``attention``  gather of a sequence's blocks into contiguous K/V and plain
-               fp64 softmax(q K^T * scale) V, one query per (sequence, head).
+               fp64 softmax(q K^T * scale) V, one query per (sequence, head),
+               or a chunk of them.
 
 Every function is pinned by ``tests/test_oracle_*.py`` against closed forms,
 invariants, a library routine (torch's CPU scaled_dot_product_attention in
@@ -34,11 +35,11 @@ here is "parity unpinned".
 """
 
 from .pool import OraclePool, PoolExhausted, RefcountError, InvalidRequest, fnv1a64, token_bytes
-from .cache_ops import oracle_append, oracle_copy_blocks
-from .attention import gather_kv, oracle_decode, oracle_decode_one
+from .cache_ops import oracle_append, oracle_copy_blocks, oracle_rope
+from .attention import gather_kv, oracle_decode, oracle_decode_one, oracle_prefill
 
 __all__ = [
     "OraclePool", "PoolExhausted", "RefcountError", "InvalidRequest", "fnv1a64", "token_bytes",
-    "oracle_append", "oracle_copy_blocks",
-    "gather_kv", "oracle_decode", "oracle_decode_one",
+    "oracle_append", "oracle_copy_blocks", "oracle_rope",
+    "gather_kv", "oracle_decode", "oracle_decode_one", "oracle_prefill",
 ]

@@ -76,3 +76,32 @@ def oracle_decode(q, k_cache, v_cache, block_tables, context_lens, scale, seqs=N
             kv = h // group
             out[s, h] = oracle_decode_one(q[s, h], keys[:, kv, :], values[:, kv, :], scale)
     return out
+
+
+def oracle_prefill(q, k_cache, v_cache, block_tables, context_lens, q_starts, scale, causal=True):
+    """Attention of a chunk of queries per sequence, float64 result [T, Hq, D].
+
+    Rows q_starts[s] .. q_starts[s + 1] - 1 of ``q`` belong to sequence s.  With
+    ``causal`` row i of n sees the first ``context_lens[s] - n + i + 1`` tokens
+    (the chunk is the end of its context), otherwise all ``context_lens[s]``.  A
+    row that sees nothing, and a row of no sequence, is zero.
+    """
+    num_q_heads = q.shape[1]
+    block_size, num_kv_heads = k_cache.shape[1], k_cache.shape[2]
+    group = num_q_heads // num_kv_heads
+    out = np.zeros(q.shape, np.float64)
+    for s in range(len(context_lens)):
+        a, b = int(q_starts[s]), int(q_starts[s + 1])
+        if b <= a:
+            continue
+        ctx = int(context_lens[s])
+        keys, values = gather_kv(k_cache, v_cache, block_tables[s], ctx, block_size)
+        seen = [min(ctx, max(0, ctx - (b - a) + i + 1)) if causal else ctx for i in range(b - a)]
+        for h in range(num_q_heads):
+            kv = h // group
+            scores = np.asarray(q[a:b, h], np.float64) @ keys[:, kv].T * float(scale)
+            for i in range(b - a):
+                if seen[i] > 0:
+                    w = np.exp(scores[i, :seen[i]] - scores[i, :seen[i]].max())
+                    out[a + i, h] = w @ values[:seen[i], kv] / w.sum()
+    return out

@@ -41,3 +41,21 @@ def oracle_copy_blocks(k_cache, v_cache, pairs):
     for src, dst in np.asarray(pairs, dtype=np.int64).reshape(-1, 2):
         k_cache[dst] = k_cache[src]
         v_cache[dst] = v_cache[src]
+
+
+def oracle_rope(x, positions, inv_freq, pair_axis=None, interleaved=False):
+    """Rotary positions of ``x`` [T, H, D] in float64: pair i turned by positions[axis(i), t] * inv_freq[i].
+
+    ``positions`` [axes, T], ``inv_freq`` [R / 2].  Pair i is the elements
+    (i, i + R / 2), or (2i, 2i + 1) when interleaved; the rest is unchanged.
+    """
+    y = np.array(x, np.float64)
+    half = len(inv_freq)
+    for i in range(half):
+        axis = 0 if pair_axis is None else int(pair_axis[i])
+        angle = np.asarray(positions[axis], np.float64) * float(inv_freq[i])
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+        c, s = np.cos(angle)[:, None], np.sin(angle)[:, None]
+        p, q = np.array(x[:, :, a], np.float64), np.array(x[:, :, b], np.float64)
+        y[:, :, a], y[:, :, b] = p * c - q * s, q * c + p * s
+    return y

@@ -236,3 +236,35 @@ class OraclePool:
                 cow_src, cow_dst = current, fresh
         slot = table[logical] * bs + offset
         return slot, length + 1, cow_src, cow_dst
+
+    def reserve_chunk(self, table, length, count, capacity=None):
+        """``count`` calls of ``reserve_slot``; returns (slots, new_length, copy pairs).  Not all or nothing."""
+        slots, pairs = [], []
+        for _ in range(count):
+            slot, length, src, dst = self.reserve_slot(table, length, capacity)
+            slots.append(slot)
+            if src >= 0:
+                pairs.append((src, dst))
+        return slots, length, pairs
+
+    # -- compaction -------------------------------------------------------------
+
+    def compact(self):
+        """Rename the live blocks to 0..n-1; returns the (old id, new id) moves.
+
+        The k-th live block that is not among the first n ids takes the k-th
+        free id among them; each old id takes its new id's place in the free
+        list, and a registered block keeps its key under the new id.
+        """
+        live = [b for b in range(self.num_blocks) if self.refcounts[b] > 0]
+        n = len(live)
+        moves = list(zip([b for b in live if b >= n], [b for b in range(n) if self.refcounts[b] == 0]))
+        for old, new in moves:
+            self.refcounts[new], self.refcounts[old] = self.refcounts[old], 0
+            self.free_list[self.free_list.index(new)] = old
+            if old in self.block_key:
+                key, tokens = self.block_key.pop(old)
+                self.block_key[new] = (key, tokens)
+                if self.prefix_cache.get(key) == old:
+                    self.prefix_cache[key] = new
+        return moves

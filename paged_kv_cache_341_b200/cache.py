@@ -13,6 +13,10 @@ is one pass of the hot path through the C ABI:
    ``pa_decode_attention`` (split into partitions plus a merge when
    ``partition_size`` > 0).
 
+``prefill_step`` does the same for a chunk of new tokens per sequence (a prompt,
+or a piece of one), with rotary positions fused into the append when asked for,
+and ``compact`` moves the live blocks to the front of the pool.
+
 Host-to-device traffic of a step is one small transfer: the slot mapping, the
 lengths, the table entries the reservation changed (at most one per row) and
 the copy pairs, plus whatever the caller passes from host memory.  The whole
@@ -64,6 +68,9 @@ class PagedKVCache:
         self._meta_views = [self._views(self._meta_host[b]) for b in range(2)]
         self._meta_dviews = [self._views(self._meta_dev[b]) for b in range(2)]
         self._step = 0
+        # metadata of chunk steps, double-buffered and grown on demand
+        self._chunk = 0
+        self._chunk_host, self._chunk_done = [None, None], [None, None]
 
     @property
     def num_seqs(self):
@@ -196,6 +203,119 @@ class PagedKVCache:
         self.attend(q, out, scale, partition_size, workspace, tables=self.d_tables[sel], lens=self.d_lens[sel],
                     stream=stream)
         return slots, pairs
+
+    # ------------------------------------------------------- chunks of tokens
+
+    def attend_chunks(self, q, q_starts, out, scale, causal=True, tables=None, lens=None, workspace=None, stream=None):
+        """Attention of ``q_starts``' chunks of ``q`` over the rows' contexts (``pa_prefill_attention``).
+
+        ``causal=False`` is cross attention: every token sees the row's whole context (an encoder's states).
+        """
+        pa.pa_prefill_attention(q, self.k_cache, self.v_cache, self.d_tables if tables is None else tables,
+                                self.d_lens if lens is None else lens, q_starts, scale, out, causal=causal,
+                                workspace=workspace, stream=stream)
+
+    def _send(self, arrays, stream):
+        """Copy int32/int64 numpy arrays to the device in one transfer; returns their device views.
+
+        The pinned side is double-buffered and grows on demand; the device side is a fresh buffer of ``stream``.
+        """
+        offsets, total = [], 0
+        for a in arrays:
+            offsets.append(total)
+            total += -(-a.nbytes // 8) * 8
+        b = self._chunk & 1
+        self._chunk += 1
+        if self._chunk_done[b] is not None:
+            self._chunk_done[b].synchronize()             # the transfer out of this host buffer has finished
+        if self._chunk_host[b] is None or self._chunk_host[b].numel() < total:
+            self._chunk_host[b] = torch.empty(max(4096, 2 * total), dtype=torch.uint8).pin_memory()
+        host = self._chunk_host[b]
+        raw = host.numpy()
+        for a, o in zip(arrays, offsets):
+            raw[o:o + a.nbytes] = np.ascontiguousarray(a).reshape(-1).view(np.uint8)
+        with torch.cuda.stream(stream):
+            dev = torch.empty(max(total, 8), dtype=torch.uint8, device=self.device)
+            dev[:total].copy_(host[:total], non_blocking=True)
+            self._chunk_done[b] = torch.cuda.Event()
+            self._chunk_done[b].record(stream)
+        kinds = {4: torch.int32, 8: torch.int64}
+        return [dev[o:o + a.nbytes].view(kinds[a.dtype.itemsize]).view(a.shape) for a, o in zip(arrays, offsets)]
+
+    def prefill_step(self, q, k_new, v_new, out, scale, counts, rows=None, inv_freq=None, positions=None,
+                     pair_axis=None, interleaved=False, q_out=None, workspace=None, stream=None):
+        """A chunk of ``counts[i]`` new tokens for each of ``rows`` (a ``slice``, default all): reserve, copy-on-write,
+        (rotate and) append, attend.
+
+        ``q``/``out`` ([T, Hq, D]) and ``k_new``/``v_new`` ([T, Hkv, D]) hold the rows' tokens packed in row order
+        (T = sum of counts); all are CUDA tensors, and the device tables must have been uploaded once
+        (``upload_tables``).  With ``inv_freq``, queries and keys are turned by their rotary angles first
+        (``pa_rope_append``): ``positions`` int32 [axes, T] on the device, by default each token's place in its
+        sequence; the turned queries go to ``q_out`` (allocated when not given).  Returns the host slots and copy
+        pairs.  A row with count 0 takes no part.
+        """
+        stream = stream or torch.cuda.current_stream()
+        sel = slice(None) if rows is None else rows
+        r0 = sel.start or 0
+        tables, lens = self.tables[sel], self.lens[sel]
+        assert tables.flags.c_contiguous and lens.flags.c_contiguous
+        counts = np.ascontiguousarray(np.asarray(counts, np.int32))
+        total = int(counts.sum(dtype=np.int64))
+        # everything that can be refused is refused before the host tables change
+        if counts.size != lens.size or (counts.size and int(counts.min()) < 0):
+            raise ValueError("counts must have one entry >= 0 per row")
+        kv_shape = (total, self.num_kv_heads, self.head_dim)
+        if (q.dim() != 3 or q.shape[0] != total or q.shape[2] != self.head_dim or tuple(out.shape) != tuple(q.shape)
+                or tuple(k_new.shape) != kv_shape or tuple(v_new.shape) != kv_shape):
+            raise ValueError("q, out [T, Hq, D] and k_new, v_new [T, Hkv, D] must hold the sum of counts tokens")
+        for t in (q, k_new, v_new, out):
+            if not t.is_cuda or t.dtype != self.dtype:
+                raise TypeError("q, k_new, v_new and out must be CUDA tensors of the cache's dtype")
+        if q.shape[1] % self.num_kv_heads or q.shape[1] // self.num_kv_heads not in (1, 2, 4, 8):
+            raise ValueError("query heads per KV head must be 1, 2, 4 or 8")
+        before = lens.copy()
+        slots, pairs, updates = self.pool.pa_reserve_chunks(tables, lens, counts, r0)
+        starts = np.zeros(counts.size + 1, np.int32)
+        np.cumsum(counts, out=starts[1:])
+        arrays = [slots, self.lens, starts, updates, pairs]
+        if inv_freq is not None and positions is None:
+            arrays.append((np.arange(total) + np.repeat(before - starts[:-1], counts)).astype(np.int32))
+        sent = self._send(arrays, stream)
+        d_slots, d_lens, d_starts, d_upd, d_pairs = sent[:5]
+        pa.pa_update_block_tables(self.d_tables, d_upd, self.d_lens, d_lens, stream=stream)
+        self.copy_blocks(d_pairs, stream=stream)
+        if inv_freq is not None:
+            if q_out is None:
+                with torch.cuda.stream(stream):
+                    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            pa.pa_rope_append(q, k_new, v_new, sent[5] if positions is None else positions, inv_freq, d_slots,
+                              self.k_cache, self.v_cache, q_out, pair_axis=pair_axis, interleaved=interleaved,
+                              stream=stream)
+            q = q_out
+        else:
+            self.append(k_new, v_new, d_slots, stream=stream)
+        if workspace is None and total:
+            with torch.cuda.stream(stream):
+                workspace = pa.prefill_workspace(total, counts.size, q.shape[1], self.num_kv_heads, self.head_dim,
+                                                 self.max_blocks, self.block_size, device=self.device)
+        self.attend_chunks(q, d_starts, out, scale, tables=self.d_tables[sel], lens=self.d_lens[sel],
+                           workspace=workspace, stream=stream)
+        return slots, pairs
+
+    def compact(self, layers=(), stream=None):
+        """Move the live blocks to the front of the pool, on the host and the device.
+
+        ``layers``: (k_cache, v_cache) pairs of further layers that share this cache's pool and tables; they move
+        in the same launch.  Block tables change on both sides (the device ones must be up to date).  Returns the
+        moves (int32 [M, 2] of old and new id).
+        """
+        stream = stream or torch.cuda.current_stream()
+        moves = self.pool.pa_pool_compact(self.tables)
+        if len(moves):
+            d_moves, = self._send([moves], stream)
+            pa.pa_move_blocks([self.k_cache] + [k for k, _ in layers], [self.v_cache] + [v for _, v in layers],
+                              d_moves, self.d_tables, stream=stream)
+        return moves
 
     def engine(self, num_q_heads, partition_size=0, stream=None):
         """A native step executor (``pa.Engine``) over this cache's pool, tables and lengths.

@@ -11,6 +11,7 @@
 #include <string>
 
 #include "cache_ops.cuh"
+#include "chunk_ops.cuh"
 #include "decode.cuh"
 #include "prefix.cuh"
 #include "prefix_tc.cuh"
@@ -67,6 +68,12 @@ pa_status make_query_map(CUtensorMap* map, const void* q, int S, int Hq, int D, 
     return pa::fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled (queries) failed (" + std::to_string(r) + ")");
   return PA_OK;
 }
+
+}  // namespace
+
+#include "launch_prefill.cuh"
+
+namespace {
 
 template <typename T, int D, int G>
 pa_status launch_prefix_umma(const DecodeArgs& a, const PrefixArgs& pf, const DeviceInfo& dev) {
@@ -633,6 +640,199 @@ pa_status pa_debug_decode_stall(int64_t wait_limit_ns) {
     return pa::fail(PA_ERR_INVALID, "pa_debug_decode_stall: wait_limit_ns must be 0 or in [1e3, 2e9]");
   g_decode_stall_ns.store(wait_limit_ns, std::memory_order_relaxed);
   return pa::ok();
+}
+
+pa_status pa_rope_append(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
+                         int64_t v_stride, const int32_t* positions, int32_t num_axes, const float* inv_freq,
+                         const int32_t* pair_axis, int32_t rotary_dim, int32_t interleaved,
+                         const int64_t* slot_mapping, int32_t num_tokens, void* q_out, void* k_cache, void* v_cache,
+                         int32_t num_blocks, int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads,
+                         int32_t head_dim, pa_dtype dtype, void* stream) {
+  if (!dtype_ok(dtype)) return pa::fail(PA_ERR_INVALID, "pa_rope_append: bad dtype");
+  if (num_tokens < 0 || num_axes <= 0 || num_blocks < 0 || block_size <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+      head_dim <= 0)
+    return pa::fail(PA_ERR_INVALID, "pa_rope_append: bad sizes");
+  if (rotary_dim <= 0 || rotary_dim % 2 != 0 || rotary_dim > head_dim)
+    return pa::fail(PA_ERR_INVALID, "pa_rope_append: rotary_dim must be even and at most head_dim");
+  if (head_dim > 2 * pa::kRopeMaxHalf || num_q_heads > 65536 || num_kv_heads > 65536)
+    return pa::fail(PA_ERR_UNSUPPORTED, "pa_rope_append: head_dim up to 512 and up to 65536 heads");
+  const int e = static_cast<int>(elem_bytes(dtype));
+  if (head_dim * e % 32 != 0)
+    return pa::fail(PA_ERR_UNSUPPORTED, "pa_rope_append: head bytes must be a multiple of 32");
+  const int64_t q_row = static_cast<int64_t>(num_q_heads) * head_dim, kv_row = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row || q_stride * e % 16 != 0 || k_stride * e % 16 != 0 ||
+      v_stride * e % 16 != 0)
+    return pa::fail(PA_ERR_INVALID, "pa_rope_append: token strides must cover a row and be a multiple of 16 bytes");
+  if (num_tokens == 0) return pa::ok();
+  if (!q || !k_new || !v_new || !positions || !inv_freq || !slot_mapping || !q_out || !k_cache || !v_cache)
+    return pa::fail(PA_ERR_INVALID, "pa_rope_append: null pointer");
+  if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(q_out) || !aligned16(k_cache) ||
+      !aligned16(v_cache))
+    return pa::fail(PA_ERR_INVALID, "pa_rope_append: q, k_new, v_new, q_out and caches must be 16-byte aligned");
+  if (q == q_out && q_stride != q_row)
+    return pa::fail(PA_ERR_INVALID, "pa_rope_append: q_out may be q only when q's rows are contiguous");
+  pa::RopeParams prm;
+  prm.q = q;
+  prm.k_new = k_new;
+  prm.v_new = v_new;
+  prm.positions = positions;
+  prm.inv_freq = inv_freq;
+  prm.pair_axis = pair_axis;
+  prm.slots = slot_mapping;
+  prm.q_out = q_out;
+  prm.k_cache = k_cache;
+  prm.v_cache = v_cache;
+  prm.q_stride = q_stride;
+  prm.k_stride = k_stride;
+  prm.v_stride = v_stride;
+  prm.num_slots = static_cast<int64_t>(num_blocks) * block_size;
+  prm.num_tokens = num_tokens;
+  prm.num_axes = num_axes;
+  prm.half = rotary_dim / 2;
+  prm.num_q_heads = num_q_heads;
+  prm.num_kv_heads = num_kv_heads;
+  prm.head_dim = head_dim;
+  const bool vec = prm.half % (16 / e) == 0;
+  void (*kern)(const pa::RopeParams) = nullptr;
+  auto pick = [&](auto zero) {
+    using T = decltype(zero);
+    if (interleaved)
+      kern = vec ? pa::rope_append_kernel<T, true, true> : pa::rope_append_kernel<T, true, false>;
+    else
+      kern = vec ? pa::rope_append_kernel<T, false, true> : pa::rope_append_kernel<T, false, false>;
+  };
+  switch (dtype) {
+    case PA_F32: pick(float{}); break;
+    case PA_F16: pick(__half{}); break;
+    case PA_BF16: pick(__nv_bfloat16{}); break;
+  }
+  DeviceInfo dev;
+  pa_status st = device_info(&dev);
+  if (st != PA_OK) return st;
+  // few tokens: a token's heads over several CTAs, so that the GPU has work on every SM
+  const int items = (num_q_heads + 2 * num_kv_heads) * (head_dim * e / 32);
+  const int most = (items + pa::kRopeThreads - 1) / pa::kRopeThreads;
+  int parts = 4 * dev.sms / num_tokens;
+  parts = parts < 1 ? 1 : parts > most ? most : parts;
+  if (parts > 65535) parts = 65535;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(num_tokens, parts);
+  cfg.blockDim = dim3(pa::kRopeThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t err = cudaLaunchKernelEx(&cfg, kern, prm);
+  if (err != cudaSuccess) return cuda_fail(err, "rope_append_kernel launch");
+  return pa::ok();
+}
+
+pa_status pa_move_blocks(void* const* k_caches, void* const* v_caches, int32_t num_layers, const int32_t* moves,
+                         int32_t num_moves, int32_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                         int32_t head_dim, int32_t* block_tables, int32_t num_rows, int32_t num_cols,
+                         int32_t table_stride, pa_dtype dtype, void* stream) {
+  if (!dtype_ok(dtype)) return pa::fail(PA_ERR_INVALID, "pa_move_blocks: bad dtype");
+  if (num_layers < 0 || num_moves < 0 || num_blocks < 0 || block_size <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+      num_rows < 0 || num_cols < 0 || table_stride < num_cols)
+    return pa::fail(PA_ERR_INVALID, "pa_move_blocks: bad sizes");
+  const int64_t block_bytes =
+      static_cast<int64_t>(block_size) * num_kv_heads * head_dim * static_cast<int64_t>(elem_bytes(dtype));
+  if (block_bytes % 16 != 0 || block_bytes / 16 > INT32_MAX / 2)
+    return pa::fail(PA_ERR_UNSUPPORTED, "pa_move_blocks: block bytes must be a multiple of 16, below 16 GiB");
+  if (num_moves == 0) return pa::ok();
+  const int64_t entries = static_cast<int64_t>(num_rows) * num_cols;
+  if (!moves || (reinterpret_cast<uintptr_t>(moves) & 7) != 0 || (num_layers > 0 && (!k_caches || !v_caches)) ||
+      (entries > 0 && !block_tables))
+    return pa::fail(PA_ERR_INVALID, "pa_move_blocks: null pointer, or moves not 8-byte aligned");
+  for (int32_t i = 0; i < num_layers; ++i)
+    if (!k_caches[i] || !v_caches[i] || !aligned16(k_caches[i]) || !aligned16(v_caches[i]))
+      return pa::fail(PA_ERR_INVALID, "pa_move_blocks: caches must be non-null and 16-byte aligned");
+  pa::MoveParams prm;
+  prm.moves = reinterpret_cast<const int2*>(moves);
+  prm.num_moves = num_moves;
+  prm.num_blocks = num_blocks;
+  prm.block_vecs = static_cast<int>(block_bytes / 16);
+  prm.slices = (prm.block_vecs + pa::kMoveSliceVecs - 1) / pa::kMoveSliceVecs;
+  prm.tables = block_tables;
+  prm.table_cols = num_cols;
+  prm.table_stride = table_stride;
+  for (int32_t first = 0; first == 0 || first < num_layers; first += pa::kMoveMaxLayers) {
+    const int n = num_layers - first < pa::kMoveMaxLayers ? num_layers - first : pa::kMoveMaxLayers;
+    for (int i = 0; i < n; ++i) {
+      prm.cache[i] = static_cast<uint4*>(k_caches[first + i]);
+      prm.cache[n + i] = static_cast<uint4*>(v_caches[first + i]);
+    }
+    prm.num_caches = 2 * n;
+    prm.copy_ctas = static_cast<int64_t>(prm.num_caches) * num_moves * prm.slices;
+    // the tables are rewritten once, by the first launch
+    prm.table_entries = first == 0 ? entries : 0;
+    const int64_t ctas = prm.copy_ctas + (prm.table_entries + pa::kRemapEntries - 1) / pa::kRemapEntries;
+    if (ctas == 0) break;
+    if (ctas > INT32_MAX) return pa::fail(PA_ERR_UNSUPPORTED, "pa_move_blocks: too many bytes for one launch");
+    pa::move_blocks_kernel<<<static_cast<unsigned>(ctas), pa::kMoveThreads, 0, static_cast<cudaStream_t>(stream)>>>(prm);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "move_blocks_kernel launch");
+  }
+  return pa::ok();
+}
+
+size_t pa_prefill_workspace_size(int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                 int32_t head_dim, int32_t max_blocks_per_seq, int32_t block_size) {
+  if (num_tokens <= 0 || num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
+      head_dim <= 0 || max_blocks_per_seq <= 0 || block_size <= 0)
+    return 0;
+  const long long cap = static_cast<long long>(max_blocks_per_seq) * block_size;
+  const PrefillLayout a = prefill_layout(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, cap, pa::kPrefillRows16);
+  const PrefillLayout b = prefill_layout(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, cap, pa::kPrefillRows32);
+  return a.total > b.total ? a.total : b.total;
+}
+
+pa_status pa_prefill_attention(const void* q, const void* k_cache, const void* v_cache, int32_t num_blocks,
+                               const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                               const int32_t* q_starts, int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
+                               int32_t num_kv_heads, int32_t head_dim, int32_t block_size, float scale,
+                               int32_t causal, void* workspace, size_t workspace_bytes, void* out, pa_dtype dtype,
+                               void* stream) {
+  if (!dtype_ok(dtype)) return pa::fail(PA_ERR_INVALID, "pa_prefill_attention: bad dtype");
+  if (num_tokens < 0 || num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0)
+    return pa::fail(PA_ERR_INVALID, "pa_prefill_attention: need Hq a positive multiple of Hkv");
+  if (num_blocks <= 0 || max_blocks_per_seq <= 0 || block_size <= 0)
+    return pa::fail(PA_ERR_INVALID, "pa_prefill_attention: bad pool sizes");
+  if (head_dim != 64 && head_dim != 128)
+    return pa::fail(PA_ERR_UNSUPPORTED, "pa_prefill_attention: head_dim must be 64 or 128");
+  const int group = num_q_heads / num_kv_heads;
+  if (group != 1 && group != 2 && group != 4 && group != 8)
+    return pa::fail(PA_ERR_UNSUPPORTED, "pa_prefill_attention: Hq/Hkv must be 1, 2, 4 or 8");
+  if (block_size != 8 && block_size % 16 != 0)
+    return pa::fail(PA_ERR_UNSUPPORTED, "pa_prefill_attention: block_size must be 8 or a multiple of 16");
+  if (static_cast<long long>(num_blocks) * block_size >= (1ll << 31) ||
+      static_cast<long long>(max_blocks_per_seq) * block_size >= (1ll << 31) - pa::kStepTokens)
+    return pa::fail(PA_ERR_INVALID, "pa_prefill_attention: pool or table too large for 32-bit token indices");
+  if (static_cast<long long>(num_tokens) * num_q_heads >= (1ll << 31))
+    return pa::fail(PA_ERR_INVALID, "pa_prefill_attention: too many query rows for 32-bit indices");
+  if (!(scale == scale) || scale > 3.0e38f || scale < -3.0e38f)
+    return pa::fail(PA_ERR_INVALID, "pa_prefill_attention: scale must be finite");
+  if (num_tokens == 0 || num_seqs == 0) return pa::ok();
+  if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !q_starts || !out)
+    return pa::fail(PA_ERR_INVALID, "pa_prefill_attention: null pointer");
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
+    return pa::fail(PA_ERR_INVALID, "pa_prefill_attention: q, caches and out must be 16-byte aligned");
+  const size_t need = pa_prefill_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                                max_blocks_per_seq, block_size);
+  if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 31) != 0)
+    return pa::fail(PA_ERR_INVALID, "pa_prefill_attention: workspace missing, too small (need " + std::to_string(need) +
+                                        " bytes) or not 32-byte aligned");
+  const PrefillArgs a{q, k_cache, v_cache, num_blocks, block_tables, max_blocks_per_seq, context_lens, q_starts,
+                      num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, scale, causal != 0,
+                      workspace, out, static_cast<cudaStream_t>(stream)};
+  switch (dtype) {
+    case PA_F32: return dispatch_prefill<float>(a);
+    case PA_F16: return dispatch_prefill<__half>(a);
+    case PA_BF16: return dispatch_prefill<__nv_bfloat16>(a);
+  }
+  return pa::fail(PA_ERR_INVALID, "pa_prefill_attention: bad dtype");
 }
 
 pa_status pa_device_error(int32_t* code_out, int32_t reset) {

@@ -247,4 +247,121 @@ pa_status pa_reserve_slots(pa_pool* pool, int32_t* tables, int32_t table_cap, in
                                        num_pairs_out, nullptr, nullptr);
 }
 
+pa_status pa_reserve_chunks(pa_pool* pool, int32_t* tables, int32_t table_cap, int32_t* lens, const int32_t* counts,
+                            int32_t num_seqs, int32_t row0, int64_t* slots_out, int32_t* pairs_out,
+                            int32_t* num_pairs_out, int32_t* updates_out, int32_t* num_updates_out) {
+  if (!pool || num_seqs < 0 || table_cap < 0 || !num_pairs_out || row0 < 0 ||
+      (num_seqs > 0 && (!tables || !lens || !counts || !slots_out || !pairs_out)) || (updates_out && !num_updates_out))
+    return pa::fail(PA_ERR_INVALID, "pa_reserve_chunks: bad argument");
+  int64_t total = 0;
+  for (int32_t s = 0; s < num_seqs; ++s) {
+    if (counts[s] < 0) return pa::fail(PA_ERR_INVALID, "pa_reserve_chunks: negative count");
+    total += counts[s];
+  }
+  // only tokens that take a block or a copy change anything but the length:
+  // those are undone one by one, the lengths at once
+  struct Step {
+    int32_t seq;
+    Undo undo;
+  };
+  std::vector<Step> steps;
+  std::vector<int32_t> old_lens;
+  try {
+    int64_t most = num_seqs;                    // blocks taken: one per started block, and a copy per sequence
+    for (int32_t s = 0; s < num_seqs; ++s) most += (counts[s] + pool->block_size - 1) / pool->block_size;
+    steps.reserve(static_cast<size_t>(most));
+    old_lens.assign(lens, lens + num_seqs);
+  } catch (...) {
+    return pa::fail(PA_ERR_INVALID, "pa_reserve_chunks: out of host memory");
+  }
+  int32_t npairs = 0, nupd = 0;
+  int64_t at = 0;
+  for (int32_t s = 0; s < num_seqs; ++s) {
+    int32_t* table = tables + static_cast<int64_t>(s) * table_cap;
+    for (int32_t i = 0; i < counts[s]; ++i) {
+      int32_t src, dst;
+      Undo u;
+      pa_status st = reserve_one(pool, table, table_cap, lens + s, slots_out + at, &src, &dst, &u);
+      if (st != PA_OK) {
+        for (size_t k = steps.size(); k-- > 0;) {
+          int32_t unused = 0;
+          roll_back(pool, tables + static_cast<int64_t>(steps[k].seq) * table_cap, &unused, steps[k].undo);
+        }
+        std::memcpy(lens, old_lens.data(), sizeof(int32_t) * num_seqs);
+        return st;
+      }
+      ++at;
+      if (src >= 0) {
+        pairs_out[2 * npairs] = src;
+        pairs_out[2 * npairs + 1] = dst;
+        ++npairs;
+      }
+      if (u.taken >= 0) {
+        steps.push_back(Step{s, u});
+        if (updates_out) {
+          updates_out[3 * nupd] = row0 + s;
+          updates_out[3 * nupd + 1] = u.logical;
+          updates_out[3 * nupd + 2] = table[u.logical];
+          ++nupd;
+        }
+      }
+    }
+  }
+  *num_pairs_out = npairs;
+  if (num_updates_out) *num_updates_out = nupd;
+  return pa::ok();
+}
+
+pa_status pa_pool_compact(pa_pool* pool, int32_t* tables, int32_t table_cap, int32_t num_rows, int32_t* moves_out,
+                          int32_t* num_moves_out) {
+  if (!pool || table_cap < 0 || num_rows < 0 || !num_moves_out || (!tables && num_rows > 0 && table_cap > 0))
+    return pa::fail(PA_ERR_INVALID, "pa_pool_compact: bad argument");
+  const int32_t nb = pool->num_blocks, live = nb - pool->count;
+  std::vector<int32_t> to;                      // where each block goes, -1: it stays
+  try {
+    to.assign(nb, -1);
+  } catch (...) {
+    return pa::fail(PA_ERR_INVALID, "pa_pool_compact: out of host memory");
+  }
+  // the k-th live block at or behind `live` goes to the k-th free block before it
+  int32_t n = 0;
+  for (int32_t src = live, dst = 0; src < nb; ++src) {
+    if (pool->refcount[src] == 0) continue;
+    while (pool->refcount[dst] != 0) ++dst;
+    if (!moves_out) return pa::fail(PA_ERR_INVALID, "pa_pool_compact: moves_out is NULL");
+    moves_out[2 * n] = src;
+    moves_out[2 * n + 1] = dst;
+    to[src] = dst++;
+    ++n;
+  }
+  // from here on nothing fails
+  for (int32_t i = 0; i < n; ++i) {
+    const int32_t src = moves_out[2 * i], dst = moves_out[2 * i + 1];
+    pool->refcount[dst] = pool->refcount[src];
+    pool->refcount[src] = 0;
+    to[dst] = src;                              // (free ids are in no table: used for the free list below)
+    if (pool->prefix_cache && pool->registered[src]) {
+      pool->hash_of[dst] = pool->hash_of[src];
+      pool->registered[dst] = 1;
+      pool->registered[src] = 0;
+      auto it = pool->by_hash.find(pool->hash_of[src]);
+      if (it != pool->by_hash.end() && it->second == src) it->second = dst;
+      std::memcpy(&pool->tokens_of[static_cast<size_t>(dst) * pool->block_size],
+                  &pool->tokens_of[static_cast<size_t>(src) * pool->block_size], sizeof(int32_t) * pool->block_size);
+    }
+  }
+  // the vacated block takes its destination's place in the free list
+  for (int32_t i = 0, idx = pool->head; i < pool->count; ++i) {
+    const int32_t b = pool->ring[idx];
+    if (to[b] >= 0) pool->ring[idx] = to[b];
+    idx = (idx + 1 == nb) ? 0 : idx + 1;
+  }
+  for (int64_t i = 0; i < static_cast<int64_t>(num_rows) * table_cap; ++i) {
+    const int32_t b = tables[i];
+    if (b >= live && b < nb && to[b] >= 0) tables[i] = to[b];
+  }
+  *num_moves_out = n;
+  return pa::ok();
+}
+
 }  // extern "C"

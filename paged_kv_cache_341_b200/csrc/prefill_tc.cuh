@@ -1,0 +1,596 @@
+// Chunk attention on the fifth-generation tensor cores (tcgen05 + tensor
+// memory), 16-bit caches.
+//
+// out[t][h] = sum_j softmax_j(scale q[t][h] . K[j]) V[j] over the context
+// tokens j < lim(t), in one pass over the context: per step of 128 tokens
+// S = Q K^T, m = running row maximum, P = 2^(S scale log2(e) - m), O += P V,
+// l += sum P; out = O / l.
+//
+// One CTA per SM (it holds all the tensor memory) takes units of the work list
+// (prefill_plan.cuh): 256 query rows of one KV head as two tiles of 128, and a
+// range of context steps.  Every K/V tile serves both query tiles.
+//
+// Roles (320 threads, so that each may hold 200 registers):
+//   warps 0-7   softmax, four warps per query tile, one thread per row (=
+//               tensor-memory lane): the whole row of 128 scores is read into
+//               registers once, so that the row maximum needs no exchange;
+//               P is rounded to the cache's type and written over S.
+//   warp 8      TMA producer: Q tiles, then K and V tiles alternately through
+//               one ring.  A piece of a cache block (8, 16, ... 128 tokens) is
+//               one box of a 5-D view of the cache that puts the D/64 column
+//               panels of 8 tokens behind one another (1024-byte atoms,
+//               128-byte swizzled), so a tile of 128 tokens is 8 copies for
+//               blocks of 16.
+//   warp 9      issues the MMAs (one thread).
+// Tensor memory: query tile g owns columns 256 g..: S (and P over it) 0..127,
+// O 128...  Products issued by one thread complete in order, so S_g(t+1) may
+// overwrite P_g(t) once PV_g(t) is issued before it, and when S_g(t) is
+// reported ready, PV_g(t-1) has completed and O may be rescaled.  While one
+// query tile's softmax runs, the tensor core works for the other.  P is handed
+// over in two halves, so that PV starts before the second half is written.
+//
+// The reference maximum of a row moves only when a score passes it by 2^kTau
+// (then the thread rescales its row of O), which the final division undoes
+// exactly; weights stay below 2^kTau, far from overflow.  S, O and the
+// statistics are float32; P is rounded to the cache's type for the second
+// product (its sum is taken before the rounding, whose errors are unbiased).
+// Of every 16 exponentials kChunkPolyExp go to the FMA pipe as a polynomial
+// (relative error 7.5e-5, below half a unit of P in either type): MUFU alone
+// would take as long as both products.
+//
+// Masks are compared only in steps that hold a masked token for some row of
+// the tile; such tokens get weight zero whatever K holds.  V rows behind the
+// context's end are zeroed in shared memory (a weight of zero would not undo
+// a NaN there).  Every wait is bounded in time.
+#ifndef PAGEDATTN_PREFILL_TC_CUH
+#define PAGEDATTN_PREFILL_TC_CUH
+
+#include <cuda.h>
+#include <cstdint>
+#include <type_traits>
+
+#include "prefill.cuh"
+#include "prefill_plan.cuh"
+#include "prefix_tc.cuh"
+#include "tcgen05.cuh"
+
+namespace pa {
+
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
+                                            int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// 32 bytes to global memory: one store when `wide` (the address is then 32-byte
+// aligned), else two of 16 bytes.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+constexpr int kChunkThreads = 320;
+constexpr int kChunkStages = 5;                  // K/V tiles in flight
+#ifndef PA_CHUNK_POLY_EXP
+#define PA_CHUNK_POLY_EXP 6
+#endif
+constexpr int kChunkPolyExp = PA_CHUNK_POLY_EXP;
+static_assert(kChunkPolyExp % 2 == 0 && kChunkPolyExp >= 0 && kChunkPolyExp <= 16, "pairs of exponentials");
+constexpr int kChunkGroupBars = 6;
+
+template <int D>
+__host__ __device__ constexpr size_t prefill_umma_smem_bytes() {
+  const size_t n = 1024 + 2 * static_cast<size_t>(D / 64) * 128 * 128            // Q tiles
+                   + kChunkStages * static_cast<size_t>(D / 64) * 128 * 128      // K/V ring
+                   + 512;                                                        // barriers
+  return n < kUmmaMinSmem ? kUmmaMinSmem : n;
+}
+
+// Steps of query tile g of a unit: [step0, end); the limit of its first and last row.
+struct ChunkTile {
+  int end, lim_first, lim_last;
+  bool any;                                      // it has rows
+};
+__device__ __forceinline__ ChunkTile chunk_tile(const PrefillEntry& e, int g, int group, int causal) {
+  ChunkTile c;
+  const int per = 128 / group;
+  const int first = g * per, last = min(e.ntok, first + per) - 1;
+  c.any = first < e.ntok;
+  c.lim_first = causal ? min(e.ctx, e.lim0 + first) : e.ctx;
+  c.lim_last = causal ? min(e.ctx, e.lim0 + last) : e.ctx;
+  c.end = c.any ? max(e.step0, min(e.step1, (max(c.lim_last, 0) + kStepTokens - 1) / kStepTokens)) : e.step0;
+  return c;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const __grid_constant__ CUtensorMap tm_q, const PrefillParams prm, const int piece_rows) {
+  static_assert(sizeof(T) == 2 && (D == 64 || D == 128), "16-bit caches, head_dim 64 or 128");
+  constexpr int kHalves = D / 64;
+  constexpr uint32_t kAtomRow = kHalves * 1024;          // 8 tokens, all panels
+  constexpr uint32_t kTileBytes = 16 * kAtomRow;         // 128 tokens
+  constexpr uint32_t kQPanel = 128 * 128;
+  constexpr uint32_t kQBytes = kHalves * kQPanel;
+  constexpr int NS = kChunkStages;
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  using M = MmaType<T>;
+
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uintptr_t base = (reinterpret_cast<uintptr_t>(smem) + 1023) & ~static_cast<uintptr_t>(1023);
+  unsigned char* s_q = reinterpret_cast<unsigned char*>(base);          // [tile][panel][128 rows][128 B]
+  unsigned char* s_kv = s_q + 2 * kQBytes;                              // [stage][token / 8][panel][8][128 B]
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_kv + NS * static_cast<size_t>(kTileBytes));
+  uint64_t* empty = full + NS;
+  uint64_t* grp = empty + NS;
+  auto s_full = [&](int g) { return grp + kChunkGroupBars * g; };       // S ready
+  auto p_half = [&](int g) { return grp + kChunkGroupBars * g + 1; };   // P of the first 64 tokens ready, O rescaled
+  auto p_full = [&](int g) { return grp + kChunkGroupBars * g + 2; };   // the rest of P
+  auto o_done = [&](int g) { return grp + kChunkGroupBars * g + 3; };   // a unit's last PV
+  auto o_free = [&](int g) { return grp + kChunkGroupBars * g + 4; };   // O read out
+  uint64_t* q_full = grp + kChunkGroupBars * 2;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* tail = q_full + 2;
+  uint64_t* drain = q_full + 3;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 4);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int G = prm.group;
+  allow_dependent_launch();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(s_full(g), 1);
+      mbar_init(p_half(g), 4);                   // one arrival per softmax warp
+      mbar_init(p_full(g), 4);
+      mbar_init(o_done(g), 1);
+      mbar_init(o_free(g), 4);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(tail, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) {
+    tc::tmem_alloc(tmem_slot, kUmmaTmemCols);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  wait_prerequisite_grids();
+  const long long units = static_cast<long long>(prm.header->num_entries) * prm.num_kv_heads;
+  // unit of round r, -1 past the last
+  auto unit_of = [&](int r) {
+    const long long u = prefill_snake(r, blockIdx.x, gridDim.x);
+    return u < units ? static_cast<int>(u) : -1;
+  };
+  const int rounds = static_cast<int>((units + gridDim.x - 1) / gridDim.x);
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      prefetch_tensormap(&tm_k);
+      prefetch_tensormap(&tm_v);
+      prefetch_tensormap(&tm_q);
+    }
+    const int BS = prm.block_size;
+    const int pieces = kStepTokens / piece_rows;           // 1..16 copies per tile
+    int st = 0;
+    uint32_t ph = 0;
+    int armed = 0;                                         // tiles whose copies were issued
+    int loaded = 0;                                        // units whose Q was loaded
+    int tails = 0;
+    bool ok = true;
+    for (int r = 0; ok && r < rounds; ++r) {
+      const int u = unit_of(r);
+      if (u < 0) continue;
+      int h;
+      const PrefillEntry en = prefill_unit(prm, u, &h);
+      const ChunkTile c0 = chunk_tile(en, 0, G, prm.causal), c1 = chunk_tile(en, 1, G, prm.causal);
+      const int end = max(c0.end, c1.end);
+      if (end <= en.step0) continue;
+      // Q, once the last S of the unit before has completed
+      if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (loaded & 1) ^ 1, abort_flag))) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(q_full, (c1.any ? 2 : 1) * kQBytes);
+        for (int g = 0; g < (c1.any ? 2 : 1); ++g)
+          for (int hf = 0; hf < kHalves; ++hf)
+            tma_load_4d(s_q + g * kQBytes + hf * kQPanel, &tm_q, q_full, 0, hf, h * G, en.tok0 + g * (128 / G));
+      }
+      __syncwarp();
+      ++loaded;
+      const int32_t* table = prm.block_tables + static_cast<int64_t>(en.seq) * prm.max_blocks;
+      // first cache row / 8 of this lane's piece of step t
+      auto piece_row = [&](int t) {
+        const int tok = t * kStepTokens + lane * piece_rows;
+        if (lane >= pieces || tok >= en.ctx) return 0;
+        const int b = tok / BS;
+        int phys = __ldg(table + b);
+        if (phys < 0 || phys >= prm.num_blocks) {
+          set_device_error(DEVERR_BAD_BLOCK_ID);
+          phys = 0;
+        }
+        return (phys * BS + (tok - b * BS)) >> 3;
+      };
+      int next = piece_row(en.step0);
+      for (int t = en.step0; ok && t < end; ++t) {
+        const int ntok = min(kStepTokens, en.ctx - t * kStepTokens);      // >= 1
+        const int n = (ntok + piece_rows - 1) / piece_rows;
+        const uint32_t tx = static_cast<uint32_t>(n) * (piece_rows / 8) * kAtomRow;
+        const int row8 = next;
+        if (t + 1 < end) next = piece_row(t + 1);
+        for (int kv = 0; kv < 2; ++kv) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1, abort_flag))) {
+            ok = false;
+            break;
+          }
+          unsigned char* dst = s_kv + static_cast<size_t>(st) * kTileBytes;
+          // the last V tile of a context lands on a barrier of its own first:
+          // the rows behind the context's end are zeroed before it is handed on
+          const bool fix = kv == 1 && ntok < kStepTokens;
+          uint64_t* bar = fix ? tail : &full[st];
+          if (lane == 0) mbar_arrive_expect_tx(bar, tx);
+          __syncwarp();
+          if (lane < n)
+            tma_load_5d(dst + lane * (piece_rows / 8) * kAtomRow, kv ? &tm_v : &tm_k, bar, 0, 0, 0, row8, h);
+          if (fix) {
+            // (the copies are in flight whatever happens to the other warps: wait for them alone)
+            if (!__all_sync(0xffffffffu, mbar_wait_drain(tail, tails & 1))) ok = false;
+            ++tails;
+            // 16-byte chunks of rows ntok..127: atom row, panel, row, chunk
+            for (int i = lane; i < (kStepTokens - ntok) * kHalves * 8; i += 32) {
+              const int row = ntok + i / (kHalves * 8), c = i % (kHalves * 8);
+              *reinterpret_cast<uint4*>(dst + (row >> 3) * kAtomRow + (c >> 3) * 1024 + (row & 7) * 128 +
+                                        (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[st]);
+          }
+          ++armed;
+          if (++st == NS) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+    }
+    // copies still in flight must land before the CTA may exit
+    if (lane == 0) {
+      for (int k = 0; k < min(armed, NS); ++k) {
+        if (--st < 0) {
+          st = NS - 1;
+          ph ^= 1;
+        }
+        mbar_wait_drain(&full[st], ph);
+      }
+      if (loaded > 0) mbar_wait_drain(q_full, (loaded - 1) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // --------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = tc::idesc_f16<kBf16>(128, 128, false, false);
+      constexpr uint32_t idesc_o = tc::idesc_f16<kBf16>(128, D, false, true);
+      const uint64_t q_desc = tc::smem_desc_sw128(smem_addr(s_q), 16, 1024);
+      const uint64_t k_desc = tc::smem_desc_sw128(smem_addr(s_kv), 16, kAtomRow);
+      const uint64_t v_desc = tc::smem_desc_sw128(smem_addr(s_kv), 1024, kAtomRow);
+      bool ok = true;
+      int st = 0;
+      uint32_t ph = 0;
+      int units_g[2] = {0, 0}, tiles_g[2] = {0, 0};
+      int loaded = 0;
+      auto issue_s = [&](int g, int ks) {
+        const uint64_t kb = k_desc + ((ks * kTileBytes) >> 4);
+        const uint64_t qb = q_desc + ((g * kQBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc::mma_f16_ss(tmem + g * kUmmaGroupCols + kSCol, qb + (((kk >> 2) * kQPanel + (kk & 3) * 32) >> 4),
+                         kb + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
+        tc::commit(s_full(g));
+      };
+      auto issue_pv = [&](int g, int vs, int half, bool first) {
+        const uint64_t vb = v_desc + ((vs * kTileBytes) >> 4);
+        const uint32_t col = tmem + g * kUmmaGroupCols;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int kk = half * 4 + k;
+          tc::mma_f16_ts(col + kOCol, col + kSCol + kk * 8, vb + ((kk * 2 * kAtomRow) >> 4), idesc_o, !first || k > 0);
+        }
+      };
+      auto advance = [&]() {
+        if (++st == NS) {
+          st = 0;
+          ph ^= 1;
+        }
+      };
+      for (int r = 0; ok && r < rounds; ++r) {
+        const int u = unit_of(r);
+        if (u < 0) continue;
+        int h;
+        const PrefillEntry en = prefill_unit(prm, u, &h);
+        int ends[2];
+        ends[0] = chunk_tile(en, 0, G, prm.causal).end;
+        ends[1] = chunk_tile(en, 1, G, prm.causal).end;
+        const int end = max(ends[0], ends[1]);
+        if (end <= en.step0) continue;
+        ok = mbar_wait(q_full, loaded & 1, abort_flag) && mbar_wait(&full[st], ph, abort_flag);
+        if (!ok) break;
+        ++loaded;
+        tc::fence_after_sync();
+        for (int g = 0; g < 2; ++g)
+          if (ends[g] > en.step0) issue_s(g, st);
+        tc::commit(&empty[st]);
+        advance();
+        if (end == en.step0 + 1) tc::commit(q_empty);
+        for (int t = en.step0; ok && t < end; ++t) {
+          const bool more = t + 1 < end;
+          const int vs = st;
+          ok = mbar_wait(&full[vs], ph, abort_flag);
+          if (!ok) break;
+          advance();
+          bool k_ready = false;
+          for (int g = 0; g < 2; ++g) {
+            if (t >= ends[g]) continue;
+            // the first product of a unit overwrites O: the unit before has read it out
+            ok = mbar_wait(p_half(g), tiles_g[g] & 1, abort_flag) &&
+                 (t > en.step0 || units_g[g] == 0 || mbar_wait(o_free(g), (units_g[g] - 1) & 1, abort_flag));
+            if (!ok) break;
+            tc::fence_after_sync();
+            issue_pv(g, vs, 0, t == en.step0);
+            ok = mbar_wait(p_full(g), tiles_g[g] & 1, abort_flag);
+            if (!ok) break;
+            ++tiles_g[g];
+            tc::fence_after_sync();
+            issue_pv(g, vs, 1, false);
+            if (t + 1 < ends[g]) {
+              if (!k_ready) {
+                ok = mbar_wait(&full[st], ph, abort_flag);
+                if (!ok) break;
+                k_ready = true;
+                tc::fence_after_sync();
+              }
+              issue_s(g, st);                    // overwrites P_g(t) after PV_g(t), in issue order
+            } else {
+              tc::commit(o_done(g));
+              ++units_g[g];
+            }
+          }
+          if (!ok) break;
+          tc::commit(&empty[vs]);
+          if (more) {
+            tc::commit(&empty[st]);
+            advance();
+            if (t + 2 == end) tc::commit(q_empty);         // the unit's last S was issued
+          }
+        }
+      }
+      // every product issued above completes before the tensor memory goes
+      tc::commit(drain);
+      mbar_wait_drain(drain, 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- softmax
+    const int g = warp >> 2;                               // query tile
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;                   // tensor-memory lane = row of the tile
+    const uint32_t t_lane = tmem + g * kUmmaGroupCols + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t s_col = t_lane + kSCol, o_col = t_lane + kOCol;
+    const bool negative = prm.qk_scale < 0.f;
+    const float qk = fabsf(prm.qk_scale);
+    const bool wide = (reinterpret_cast<uintptr_t>(prm.out) & 31) == 0;
+    int tiles = 0, done = 0;
+    bool ok = true;
+    for (int r = 0; ok && r < rounds; ++r) {
+      const int u = unit_of(r);
+      if (u < 0) continue;
+      int h;
+      const PrefillEntry en = prefill_unit(prm, u, &h);
+      const ChunkTile ct = chunk_tile(en, g, G, prm.causal);
+      const int tok = (g * 128 + row) / G;                 // token of this row in the unit
+      const int head = row % G;
+      const bool valid = tok < en.ntok;
+      const int lim = prm.causal ? min(en.ctx, en.lim0 + min(tok, en.ntok - 1)) : en.ctx;
+      float m = -INFINITY;
+      float2 l2 = make_float2(0.f, 0.f);
+      for (int t = en.step0; t < ct.end; ++t, ++tiles) {
+        if (!__all_sync(0xffffffffu, mbar_wait(s_full(g), tiles & 1, abort_flag))) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        uint32_t x[128];
+        tc::tmem_ld32_at<0>(s_col, x);
+        tc::tmem_ld32_at<32>(s_col + 32, x);
+        tc::tmem_ld32_at<64>(s_col + 64, x);
+        tc::tmem_ld32_at<96>(s_col + 96, x);
+        tc::tmem_wait_ld();
+        if (negative) {
+#pragma unroll
+          for (int j = 0; j < 128; ++j) x[j] ^= 0x80000000u;
+        }
+        const int nv = lim - t * kStepTokens;              // tokens of this step the row sees
+        const bool masked = ct.lim_first < (t + 1) * kStepTokens;       // uniform over the tile
+        float mul = qk;
+        if (masked) {
+          mul = 1.f;                                       // scaled here: 0 * inf must not reach the weights
+#pragma unroll
+          for (int j = 0; j < 128; ++j)
+            x[j] = j < nv ? __float_as_uint(__uint_as_float(x[j]) * qk) : 0xff800000u;
+        }
+        float cm[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          cm[k] = fmaxf(__uint_as_float(x[k]), __uint_as_float(x[4 + k]));
+#pragma unroll
+          for (int j = 8; j < 128; j += 8)
+            cm[k] = fmax3(cm[k], __uint_as_float(x[j + k]), __uint_as_float(x[j + 4 + k]));
+        }
+        const float c = fmaxf(fmax3(cm[0], cm[1], cm[2]), cm[3]) * mul;
+        if (__any_sync(0xffffffffu, c > m + kTau)) {
+          const float mn = c > m + kTau ? c : m;
+          const float f = mn != m ? exp2_approx(m - mn) : 1.f;     // 0 when m was -inf
+          if (t > en.step0) {
+#pragma unroll 1
+            for (int ob = 0; ob < D / 16; ++ob) {
+              uint32_t o[16];
+              tc::tmem_ld16(o_col + ob * 16, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tc::tmem_st16(o_col + ob * 16, o);
+            }
+          }
+          l2.x *= f;
+          l2.y *= f;
+          m = mn;
+        }
+        const float mu = m == -INFINITY ? 0.f : m;         // nothing visible yet: every weight is 2^-inf
+        const float2 nm2 = make_float2(-mu, -mu), mul2 = make_float2(mul, mul);
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int q32 = 0; q32 < 4; ++q32) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int j = q32 * 32 + 2 * i;
+            float2 e = nm2;
+            ffma2(e, make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), mul2);
+            x[j] = __float_as_uint(e.x);
+            x[j + 1] = __float_as_uint(e.y);
+          }
+          if (masked) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              x[q32 * 32 + j] = __float_as_uint(exp2_approx(__uint_as_float(x[q32 * 32 + j])));
+          } else {
+#pragma unroll
+            for (int b = 0; b < 32; b += 16) {
+#pragma unroll
+              for (int j = 0; j < 16 - kChunkPolyExp; ++j)
+                x[q32 * 32 + b + j] = __float_as_uint(exp2_approx(__uint_as_float(x[q32 * 32 + b + j])));
+#pragma unroll
+              for (int j = 16 - kChunkPolyExp; j < 16; j += 2) {
+                const int k = q32 * 32 + b + j;
+                const float2 y = exp2_poly2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
+                x[k] = __float_as_uint(y.x);
+                x[k + 1] = __float_as_uint(y.y);
+              }
+            }
+          }
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int j = q32 * 32 + 2 * i;
+            const float2 y = make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+            w[i] = M::pack(y.x, y.y);
+            fadd2(ls[i & 1], y);
+          }
+          tc::tmem_st16(s_col + q32 * 16, w);
+          if (q32 == 1 || q32 == 3) {
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q32 == 1 ? p_half(g) : p_full(g));
+          }
+        }
+        fadd2(l2, ls[0]);
+        fadd2(l2, ls[1]);
+      }
+      if (!ok) break;
+      const float l = l2.x + l2.y;
+      const bool have = ct.end > en.step0;                 // O holds this unit's product
+      if (have) {
+        if (!__all_sync(0xffffffffu, mbar_wait(o_done(g), done & 1, abort_flag))) {
+          ok = false;
+          break;
+        }
+        ++done;
+        tc::fence_after_sync();
+      }
+      if (en.slot >= 0) {
+        const int64_t at = (static_cast<int64_t>(en.slot) * prm.num_kv_heads + h) * kPrefillRows16 + g * 128 + row;
+        if (valid) prm.part_ml[at] = make_float2(m, l);
+        if (have) {
+#pragma unroll
+          for (int cb = 0; cb < D / 32; ++cb) {
+            uint32_t o[32];
+            tc::tmem_ld32(o_col + cb * 32, o);
+            tc::tmem_wait_ld();
+            if (valid) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 8) {
+                const uint32_t w[8] = {o[j], o[j + 1], o[j + 2], o[j + 3], o[j + 4], o[j + 5], o[j + 6], o[j + 7]};
+                store32(prm.part_acc + at * D + cb * 32 + j, w, true);
+              }
+            }
+          }
+        }
+      } else {
+        T* dst = static_cast<T*>(prm.out) +
+                 (static_cast<int64_t>(en.tok0 + tok) * prm.num_kv_heads * G + h * G + head) * D;
+        const float inv = l == 0.f ? 0.f : 1.f / l;        // a row that sees nothing is zero
+#pragma unroll
+        for (int cb = 0; cb < D / 32; ++cb) {
+          uint32_t o[32];
+          if (have) {
+            tc::tmem_ld32(o_col + cb * 32, o);
+            tc::tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = 0u;
+          }
+          if (valid) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 16) {
+              uint32_t w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                w[i] = M::pack(__uint_as_float(o[j + 2 * i]) * inv, __uint_as_float(o[j + 2 * i + 1]) * inv);
+              store32(dst + cb * 32 + j, w, wide);
+            }
+          }
+        }
+      }
+      if (have) {
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_free(g));
+      }
+    }
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 9) {
+    __syncwarp();
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kUmmaTmemCols);
+  }
+}
+
+}  // namespace pa
+
+#endif

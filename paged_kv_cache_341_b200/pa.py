@@ -63,6 +63,15 @@ SIGNATURES = {
     "pa_shared_prefix_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32]),
     "pa_decode_attention_shared_prefix": (_i32, [_vp, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _vp, _i32, _i32,
                                                  _i32, _i32, _i32, _f32, _i32, _vp, _sz, _vp, _i32, _vp]),
+    "pa_reserve_chunks": (_i32, [_vp, _p32, _i32, _p32, _p32, _i32, _i32, _p64, _p32, _p32, _p32, _p32]),
+    "pa_pool_compact": (_i32, [_vp, _p32, _i32, _i32, _p32, _p32]),
+    "pa_rope_append": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp,
+                              _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp]),
+    "pa_move_blocks": (_i32, [ctypes.POINTER(_vp), ctypes.POINTER(_vp), _i32, _vp, _i32, _i32, _i32, _i32, _i32, _vp,
+                              _i32, _i32, _i32, _i32, _vp]),
+    "pa_prefill_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32]),
+    "pa_prefill_attention": (_i32, [_vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
+                                    _f32, _i32, _vp, _sz, _vp, _i32, _vp]),
     "pa_device_error": (_i32, [_p32, _i32]),
     "pa_debug_decode_stall": (_i32, [_i64]),
     "pa_debug_last_prefix_kernel": (_i32, []),
@@ -227,6 +236,44 @@ class Pool:
                                                   ctypes.byref(nupd)))
         return npairs.value, nupd.value
 
+    def pa_reserve_chunks(self, tables, lens, counts, row0=0):
+        """``counts[s]`` tokens for every row of ``tables`` ([S, cap] int32, in place) and ``lens`` ([S] int32, in place).
+
+        Returns (slots int64 [sum of counts], pairs int32 [P, 2], updates int32 [U, 3]): the slots packed in
+        row order, the copy-on-write pairs, and the table entries written as (row0 + s, column, block id).
+        """
+        if tables.dtype != np.int32 or lens.dtype != np.int32 or not (tables.flags.c_contiguous and
+                                                                      lens.flags.c_contiguous):
+            raise TypeError("tables and lens must be contiguous int32 arrays")
+        counts, cptr = _i32_array(counts)
+        if tables.ndim != 2 or tables.shape[0] != lens.size or counts.size != lens.size:
+            raise ValueError("tables, lens and counts must have one row per sequence")
+        if counts.size and int(counts.min()) < 0:
+            raise ValueError("counts must not be negative")
+        s, total = lens.size, int(counts.sum(dtype=np.int64))
+        slots = np.empty(max(total, 1), np.int64)
+        pairs = np.empty((max(s, 1), 2), np.int32)
+        updates = np.empty((int((-(-counts.astype(np.int64) // self.block_size)).sum()) + s + 1, 3), np.int32)
+        npairs, nupd = ctypes.c_int32(), ctypes.c_int32()
+        _check(_lib.pa_reserve_chunks(self._h, tables.ctypes.data_as(_p32), tables.shape[1],
+                                      lens.ctypes.data_as(_p32), cptr, s, int(row0), slots.ctypes.data_as(_p64),
+                                      pairs.ctypes.data_as(_p32), ctypes.byref(npairs),
+                                      updates.ctypes.data_as(_p32), ctypes.byref(nupd)))
+        return slots[:total], pairs[: npairs.value].copy(), updates[: nupd.value].copy()
+
+    def pa_pool_compact(self, tables=None):
+        """Rename the live blocks to 0..n-1; ``tables`` ([rows, cap] int32) is rewritten in place.
+
+        Returns the moves int32 [M, 2] of (old id, new id) to run on every layer's cache (``pa_move_blocks``).
+        """
+        if tables is not None and (tables.dtype != np.int32 or tables.ndim != 2 or not tables.flags.c_contiguous):
+            raise TypeError("tables must be a contiguous 2-D int32 array")
+        moves = np.empty((self.num_blocks // 2 + 1, 2), np.int32)
+        n = ctypes.c_int32()
+        rows, cap = (0, 0) if tables is None else tables.shape
+        _check(_lib.pa_pool_compact(self._h, None if tables is None else tables.ctypes.data_as(_p32), cap, rows,
+                                    moves.ctypes.data_as(_p32), ctypes.byref(n)))
+        return moves[: n.value].copy()
 
     # -- prefix caching ------------------------------------------------------
 
@@ -293,6 +340,142 @@ def pa_update_block_tables(block_tables, updates, context_lens=None, new_lens=No
                                        block_tables.stride(0), _dev(updates, "updates", torch.int32) if n else None,
                                        n, _dev(context_lens, "context_lens", torch.int32) if nl else None,
                                        _dev(new_lens, "new_lens", torch.int32) if nl else None, nl, _stream(stream)))
+
+
+def _on_current_device(tensors):
+    """The calls launch on the current device: refuse tensors of another one."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != cur:
+            raise ValueError("tensor on %s, but the current device is cuda:%d" % (t.device, cur))
+
+
+def _token_rows(t, name, dtype, shape):
+    """Pointer and token stride of a [T, H, D] CUDA tensor whose rows [H, D] are contiguous."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must have dtype %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    row = shape[1] * shape[2]
+    if t.shape[0] and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != shape[2])):
+        raise ValueError("%s must have contiguous token rows" % name)
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else row
+
+
+def pa_rope_append(q, k_new, v_new, positions, inv_freq, slot_mapping, k_cache, v_cache, q_out, pair_axis=None,
+                   interleaved=False, stream=None):
+    """Turn q and k_new by their rotary angles; q goes to ``q_out``, k and v to their slots.
+
+    q [T, Hq, D], k_new/v_new [T, Hkv, D] (token strides allowed); positions int32 [axes, T] or [T]; inv_freq
+    float32 [rotary_dim / 2]; slot_mapping int64 [T]; pair_axis int32 [rotary_dim / 2] (None: axis 0);
+    caches [NB, bs, Hkv, D]; q_out [T, Hq, D] (may be q).
+    """
+    nb, bs, hkv, d = k_cache.shape
+    dt = k_cache.dtype
+    t, hq = q.shape[0], q.shape[1]
+    if tuple(v_cache.shape) != tuple(k_cache.shape) or tuple(q_out.shape) != (t, hq, d):
+        raise ValueError("shape mismatch between q, q_out and caches")
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if positions.numel() != axes * t or slot_mapping.numel() != t:
+        raise ValueError("positions must be [axes, T] and slot_mapping [T]")
+    if pair_axis is not None and pair_axis.numel() != inv_freq.numel():
+        raise ValueError("pair_axis must have one entry per pair of inv_freq")
+    qp, qs = _token_rows(q, "q", dt, (t, hq, d))
+    kp, ks = _token_rows(k_new, "k_new", dt, (t, hkv, d))
+    vp, vs = _token_rows(v_new, "v_new", dt, (t, hkv, d))
+    _on_current_device((q, k_new, v_new, positions, inv_freq, pair_axis, slot_mapping, k_cache, v_cache, q_out))
+    _check(_lib.pa_rope_append(qp, qs, kp, ks, vp, vs, _dev(positions, "positions", torch.int32), axes,
+                               _dev(inv_freq, "inv_freq", torch.float32),
+                               None if pair_axis is None else _dev(pair_axis, "pair_axis", torch.int32),
+                               2 * inv_freq.numel(), 1 if interleaved else 0,
+                               _dev(slot_mapping, "slot_mapping", torch.int64), t, _dev(q_out, "q_out", dt),
+                               _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache", dt), nb, bs, hq, hkv, d,
+                               DTYPE_CODE[dt], _stream(stream)))
+
+
+def pa_move_blocks(k_caches, v_caches, moves, block_tables=None, stream=None):
+    """Run a compaction's moves on every layer's cache and rewrite the device block tables.
+
+    k_caches/v_caches: lists of [NB, bs, Hkv, D] CUDA tensors, one per layer; moves: int32 CUDA [M, 2] of
+    (source, destination), sources increasing; block_tables: int32 CUDA [rows, cols] with unit column stride.
+    """
+    k_caches, v_caches = list(k_caches), list(v_caches)
+    if not k_caches or len(k_caches) != len(v_caches):
+        raise ValueError("need as many K caches as V caches, at least one")
+    shape, dt = k_caches[0].shape, k_caches[0].dtype
+    if len({c.data_ptr() for c in k_caches + v_caches}) != 2 * len(k_caches):
+        raise ValueError("the caches must be distinct")
+    ptrs = []
+    for c in k_caches + v_caches:
+        if c.shape != shape:
+            raise ValueError("all caches must have the shape of the first")
+        ptrs.append(_dev(c, "cache", dt).value)
+    n = len(k_caches)
+    kp, vp = (_vp * n)(*ptrs[:n]), (_vp * n)(*ptrs[n:])
+    rows = cols = stride = 0
+    tp = None
+    if block_tables is not None and block_tables.numel():
+        if block_tables.dim() != 2 or block_tables.stride(1) != 1:
+            raise ValueError("block_tables must be a 2-D tensor with unit column stride")
+        if block_tables.dtype != torch.int32 or not block_tables.is_cuda:
+            raise TypeError("block_tables must be an int32 CUDA tensor")
+        rows, cols = block_tables.shape
+        stride = max(block_tables.stride(0), cols)
+        tp = ctypes.c_void_p(block_tables.data_ptr())
+    _on_current_device(k_caches + v_caches + [moves, block_tables])
+    nb, bs, hkv, d = shape
+    _check(_lib.pa_move_blocks(kp, vp, n, _dev(moves, "moves", torch.int32), moves.numel() // 2, nb, bs, hkv, d, tp,
+                               rows, cols, stride, DTYPE_CODE[dt], _stream(stream)))
+
+
+def pa_prefill_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                              block_size):
+    return int(_lib.pa_prefill_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                              max_blocks_per_seq, block_size))
+
+
+def prefill_workspace(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size,
+                      device=None):
+    """Allocate (through torch) the workspace pa_prefill_attention needs for calls of up to these sizes."""
+    nbytes = pa_prefill_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                                       block_size)
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def pa_prefill_attention(q, k_cache, v_cache, block_tables, context_lens, q_starts, scale, out, causal=True,
+                         workspace=None, stream=None):
+    """Attention of a chunk of tokens per sequence over the paged cache (causal=False: cross attention).
+
+    q, out [T, Hq, D] packed; q_starts int32 [S + 1]; caches [NB, bs, Hkv, D]; block_tables int32 [S, MB];
+    context_lens int32 [S] (with causal, including the chunk itself).  The workspace
+    (pa_prefill_workspace_size bytes) is allocated here through torch when not given.
+    """
+    t, hq, d = q.shape
+    nb, bs, hkv, d2 = k_cache.shape
+    if d2 != d or tuple(out.shape) != (t, hq, d) or tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("shape mismatch between q, caches and out")
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [S, max_blocks]")
+    s, mb = block_tables.shape
+    if context_lens.numel() != s or q_starts.numel() != s + 1:
+        raise ValueError("context_lens must be [S] and q_starts [S + 1]")
+    code = DTYPE_CODE[k_cache.dtype]
+    qp, op = _dev(q, "q", k_cache.dtype), _dev(out, "out", k_cache.dtype)
+    _on_current_device((q, k_cache, v_cache, block_tables, context_lens, q_starts, out, workspace))
+    if workspace is None:
+        # (on the stream that uses it, so that the allocator orders its reuse)
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(stream):
+            workspace = prefill_workspace(t, s, hq, hkv, d, mb, bs, device=q.device) if t and s else q
+    _check(_lib.pa_prefill_attention(qp, _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache", k_cache.dtype), nb,
+                                     _dev(block_tables, "block_tables", torch.int32), mb,
+                                     _dev(context_lens, "context_lens", torch.int32),
+                                     _dev(q_starts, "q_starts", torch.int32), t, s, hq, hkv, d, bs, float(scale),
+                                     1 if causal else 0, _dev(workspace, "workspace"),
+                                     workspace.numel() * workspace.element_size(), op, code, _stream(stream)))
 
 
 def pa_read_stream(buf, sink, stream=None):
