@@ -21,7 +21,11 @@
 //               panels of 8 tokens behind one another (1024-byte atoms,
 //               128-byte swizzled), so a tile of 128 tokens is 8 copies for
 //               blocks of 16.
-//   warp 9      issues the MMAs (one thread).
+//   warp 9      issues the MMAs: the whole warp runs the loop and one elected
+//               lane issues, so that the operands stay in uniform registers
+//               (from a single thread's branch a product was issued every 90
+//               to 100 cycles beside the busy softmax warps, and the tensor
+//               core takes 64 for one: 1,056 -> 1,289 TFLOP/s).
 // Tensor memory: query tile g owns columns 256 g..: S (and P over it) 0..127,
 // O 128...  Products issued by one thread complete in order, so S_g(t+1) may
 // overwrite P_g(t) once PV_g(t) is issued before it, and when S_g(t) is
@@ -65,6 +69,47 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// One lane of the (converged) warp: 1 in it, 0 in the others.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r;
+}
+// Products and commits issued by the lane with `one` set, in code that the whole
+// warp runs: operands stay in uniform registers.
+template <bool kAcc>
+__device__ __forceinline__ void mma_ss_one(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %4, 0;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(one), "n"(kAcc ? 1 : 0)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_one(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %4, 0;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(one), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one(uint32_t one, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(one)
+      : "memory");
+}
+
 // 32 bytes to global memory: one store when `wide` (the address is then 32-byte
 // aligned), else two of 16 bytes.
 __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wide) {
@@ -81,7 +126,7 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wi
 constexpr int kChunkThreads = 320;
 constexpr int kChunkStages = 5;                  // K/V tiles in flight
 #ifndef PA_CHUNK_POLY_EXP
-#define PA_CHUNK_POLY_EXP 6
+#define PA_CHUNK_POLY_EXP 4
 #endif
 constexpr int kChunkPolyExp = PA_CHUNK_POLY_EXP;
 static_assert(kChunkPolyExp % 2 == 0 && kChunkPolyExp >= 0 && kChunkPolyExp <= 16, "pairs of exponentials");
@@ -291,7 +336,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     __syncwarp();
   } else if (warp == 9) {
     // --------------------------------------------------------- MMA issuer
-    if (lane == 0) {
+    {
+      const uint32_t one = elect_lane();
       constexpr uint32_t idesc_s = tc::idesc_f16<kBf16>(128, 128, false, false);
       constexpr uint32_t idesc_o = tc::idesc_f16<kBf16>(128, D, false, true);
       const uint64_t q_desc = tc::smem_desc_sw128(smem_addr(s_q), 16, 1024);
@@ -306,10 +352,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const uint64_t kb = k_desc + ((ks * kTileBytes) >> 4);
         const uint64_t qb = q_desc + ((g * kQBytes) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc::mma_f16_ss(tmem + g * kUmmaGroupCols + kSCol, qb + (((kk >> 2) * kQPanel + (kk & 3) * 32) >> 4),
-                         kb + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
-        tc::commit(s_full(g));
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t qk = qb + (((kk >> 2) * kQPanel + (kk & 3) * 32) >> 4);
+          const uint64_t kk_ = kb + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4);
+          if (kk == 0) mma_ss_one<false>(one, tmem + g * kUmmaGroupCols + kSCol, qk, kk_, idesc_s);
+          else mma_ss_one<true>(one, tmem + g * kUmmaGroupCols + kSCol, qk, kk_, idesc_s);
+        }
+        commit_one(one, s_full(g));
       };
       auto issue_pv = [&](int g, int vs, int half, bool first) {
         const uint64_t vb = v_desc + ((vs * kTileBytes) >> 4);
@@ -317,7 +366,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int kk = half * 4 + k;
-          tc::mma_f16_ts(col + kOCol, col + kSCol + kk * 8, vb + ((kk * 2 * kAtomRow) >> 4), idesc_o, !first || k > 0);
+          mma_ts_one(one, col + kOCol, col + kSCol + kk * 8, vb + ((kk * 2 * kAtomRow) >> 4), idesc_o, !first || k > 0);
         }
       };
       auto advance = [&]() {
@@ -342,9 +391,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         tc::fence_after_sync();
         for (int g = 0; g < 2; ++g)
           if (ends[g] > en.step0) issue_s(g, st);
-        tc::commit(&empty[st]);
+        commit_one(one, &empty[st]);
         advance();
-        if (end == en.step0 + 1) tc::commit(q_empty);
+        if (end == en.step0 + 1) commit_one(one, q_empty);
         for (int t = en.step0; ok && t < end; ++t) {
           const bool more = t + 1 < end;
           const int vs = st;
@@ -374,21 +423,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               }
               issue_s(g, st);                    // overwrites P_g(t) after PV_g(t), in issue order
             } else {
-              tc::commit(o_done(g));
+              commit_one(one, o_done(g));
               ++units_g[g];
             }
           }
           if (!ok) break;
-          tc::commit(&empty[vs]);
+          commit_one(one, &empty[vs]);
           if (more) {
-            tc::commit(&empty[st]);
+            commit_one(one, &empty[st]);
             advance();
-            if (t + 2 == end) tc::commit(q_empty);         // the unit's last S was issued
+            if (t + 2 == end) commit_one(one, q_empty);         // the unit's last S was issued
           }
         }
       }
       // every product issued above completes before the tensor memory goes
-      tc::commit(drain);
+      commit_one(one, drain);
       mbar_wait_drain(drain, 0);
     }
     __syncwarp();
