@@ -39,14 +39,12 @@ struct PrefillArgs {
 // function of the arguments alone (a B200 has 148 SMs).
 constexpr int kPrefillMaxCtas = 148;
 
-// Workspace: [header 256 B][tile ends][entries][merges][partial (m, l)][partial outputs].
-// The sizes follow the planner's rule: over all heads, the tiles that are split
-// hold at most W = target * limit steps, so that (per head) their extra pieces
-// number at most target / Hkv, their pieces at most twice that, and they
-// themselves at most target / Hkv.
+// Workspace: [header 256 B][tile ends][tile steps][entries][merges][partial (m, l)][partial outputs].
+// There is room for kSplitUnits pieces of split contexts per CTA (over all
+// heads); the planner leaves contexts whole rather than take more.
 struct PrefillLayout {
-  size_t ends, entries, merges, ml, acc, total;
-  int max_entries, max_merges, max_slots;
+  size_t ends, steps, entries, merges, ml, acc, total;
+  int max_tiles, max_entries, max_merges, max_slots;
 };
 
 PrefillLayout prefill_layout(long long T, long long S, long long Hq, long long Hkv, long long D, long long cap,
@@ -54,16 +52,16 @@ PrefillLayout prefill_layout(long long T, long long S, long long Hq, long long H
   const long long G = Hq / Hkv;
   const long long tiles = std::min(T, S) + T * G / rows;                  // every non-empty chunk may end in a part tile
   const long long steps = (cap + pa::kStepTokens - 1) / pa::kStepTokens;
-  const long long target = static_cast<long long>(pa::kSplitUnits) * kPrefillMaxCtas;
-  const long long per_head = target / Hkv + 1;
-  const long long most = (steps + pa::kMinSplitSteps - 1) / pa::kMinSplitSteps;     // pieces of one tile
-  const bool split = most > 1;
+  const long long pieces = std::min(static_cast<long long>(pa::kSplitUnits) * kPrefillMaxCtas / Hkv, tiles * steps);
+  const bool split = steps > pa::kMinSplitSteps && pieces >= 2;
   PrefillLayout L;
-  L.max_merges = split ? static_cast<int>(std::min(per_head, tiles)) : 0;
-  L.max_slots = split ? static_cast<int>(std::min(2 * per_head, tiles * most)) : 0;
-  L.max_entries = static_cast<int>(tiles + (split ? std::min(per_head, tiles * most) : 0));
+  L.max_tiles = static_cast<int>(tiles);
+  L.max_slots = split ? static_cast<int>(pieces) : 0;
+  L.max_merges = L.max_slots / 2;                                         // a split context has two pieces at least
+  L.max_entries = L.max_tiles + L.max_slots;
   L.ends = 256;
-  L.entries = L.ends + round256(static_cast<size_t>(S) * sizeof(int));
+  L.steps = L.ends + round256(static_cast<size_t>(S) * sizeof(int));
+  L.entries = L.steps + round256(static_cast<size_t>(L.max_tiles) * sizeof(int));
   L.merges = L.entries + round256(static_cast<size_t>(L.max_entries) * sizeof(pa::PrefillEntry));
   L.ml = L.merges + round256(static_cast<size_t>(L.max_merges) * sizeof(pa::PrefillMerge));
   const size_t slot_rows = static_cast<size_t>(L.max_slots) * Hkv * rows;
@@ -152,7 +150,8 @@ pa_status launch_prefill(const PrefillArgs& a) {
   pp.causal = a.causal;
   pp.cap = a.max_blocks * a.BS;
   pp.ctas = std::min(dev.sms, kPrefillMaxCtas);
-  pp.max_entries = L.max_entries;
+  pp.max_tiles = L.max_tiles;
+  pp.tile_steps = reinterpret_cast<int*>(ws + L.steps);
   pp.max_merges = L.max_merges;
   pp.max_slots = L.max_slots;
   cfg.gridDim = dim3(1);

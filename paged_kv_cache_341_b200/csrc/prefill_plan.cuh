@@ -21,8 +21,8 @@ namespace pa {
 constexpr int kStepTokens = 128;               // context tokens per K/V step
 constexpr int kPrefillRows16 = 256;            // rows per tile, 16-bit caches (two MMA tiles of 128)
 constexpr int kPrefillRows32 = 64;             // rows per tile, float32 caches
-constexpr int kMinSplitSteps = 4;              // a piece of a split context is at least this long
-constexpr int kSplitUnits = 2;                 // pieces aimed at per CTA where contexts are split
+constexpr int kMinSplitSteps = 2;              // a piece of a split context is at least about this long
+constexpr int kSplitUnits = 2;                 // pieces of split contexts per CTA that the workspace has room for
 constexpr int kPrefillPlanThreads = 1024;
 constexpr int kPrefillBuckets = 1024;
 
@@ -55,7 +55,8 @@ struct PrefillPlanParams {
   int num_seqs, num_tokens, num_kv_heads, group, rows;
   int causal, cap;               // cap: tokens a table row can hold
   int ctas;                      // CTAs of the attention grid
-  int max_entries, max_merges, max_slots;      // slots are per KV head
+  int max_tiles, max_merges, max_slots;        // capacities; slots are per KV head
+  int* tile_steps;               // [max_tiles]
 };
 
 // Chunk of sequence s, clamped into the arrays: tokens [lo, lo + n), context.
@@ -67,21 +68,36 @@ __device__ __forceinline__ void prefill_seq(const PrefillPlanParams& p, int s, i
   *bad = *lo != a || *lo + *n != b || *ctx != c;
 }
 
+// How long the attention kernel takes for a work list, in K/V steps, from sums
+// over its pieces: every piece costs its steps and kPieceSteps for its start
+// and end, a piece of a split context also kPartialSteps for its partial; C
+// CTAs take the pieces longest first, so that no schedule beats the average,
+// and pieces of more than half of the longest share no CTA unless they fill
+// more than one round; a split call pays kMergeSteps for the merge.
+constexpr float kPieceSteps = 2.f;
+constexpr float kPartialSteps = 1.5f;
+constexpr float kMergeSteps = 3.f;
+
 // One CTA lists the work of a call, longest pieces first (a counting sort on
-// their steps), and decides where contexts are split: with W steps over all
-// heads and C CTAs, a tile of more than W / (kSplitUnits C) steps is cut into
-// equal pieces of at most that many (and at least kMinSplitSteps), so that few
-// rows over a long context still fill the GPU, while calls with plenty of
-// tiles are not split at all.  The order of entries within a bucket and of the
-// partial slots depends on the order of atomics; no result does (each piece
-// has its own slot, and a merge reads its pieces in order).
+// their steps), and decides where contexts are split: 32 limits on the steps of
+// a piece (the longest context over 1, 2, .. 16, and over the numbers that make
+// 1 to 16 full rounds of the CTAs) are weighed by the estimate above, one per
+// warp, and the cheapest is taken, so that few rows over a long context fill
+// the GPU while calls with plenty of tiles are not split at all.  The order of
+// entries within a bucket and of the partial slots depends on the order of
+// atomics; no result does (each piece has its own slot, and a merge reads its
+// pieces in order).  Bound by the latency of its few dependent loads.
 __global__ void __launch_bounds__(kPrefillPlanThreads) prefill_plan_kernel(const PrefillPlanParams p) {
   __shared__ int s_warp[32];
   __shared__ int s_hist[kPrefillBuckets];
-  __shared__ unsigned long long s_work;
+  __shared__ float s_est[32];
+  __shared__ int s_limit[32];
   __shared__ int s_base, s_max, s_slots, s_merges, s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   allow_dependent_launch();
+  if (tid == 0) s_base = s_max = s_slots = s_merges = s_bad = 0;
+  s_hist[tid] = 0;
+  static_assert(kPrefillBuckets == kPrefillPlanThreads, "one bucket per thread");
   wait_prerequisite_grids();
 
   // inclusive scan of one int per thread over the CTA; *total = the sum
@@ -107,14 +123,7 @@ __global__ void __launch_bounds__(kPrefillPlanThreads) prefill_plan_kernel(const
     return r;
   };
 
-  if (tid == 0) {
-    s_work = 0;
-    s_base = s_max = s_slots = s_merges = s_bad = 0;
-  }
-  for (int i = tid; i < kPrefillBuckets; i += kPrefillPlanThreads) s_hist[i] = 0;
-  __syncthreads();
-
-  // tiles of the sequences before each one
+  // tiles of sequences 0 .. s
   for (int s0 = 0; s0 < p.num_seqs; s0 += kPrefillPlanThreads) {
     const int s = s0 + tid;
     int tiles = 0;
@@ -126,15 +135,14 @@ __global__ void __launch_bounds__(kPrefillPlanThreads) prefill_plan_kernel(const
       tiles = static_cast<int>((static_cast<long long>(n) * p.group + p.rows - 1) / p.rows);
     }
     int total;
-    const int incl = scan(tiles, &total) + s_base;
+    const int before = s_base;
+    const int incl = scan(tiles, &total) + before;
     if (s < p.num_seqs) p.tile_ends[s] = incl;
-    __syncthreads();
-    if (tid == 0) s_base += total;
+    if (tid == 0) s_base = before + total;
     __syncthreads();
   }
   // disjoint chunks fill the list exactly; overlapping ones (an error) are cut off
-  if (s_base > p.max_entries) s_bad = 1;
-  const int tiles = min(s_base, p.max_entries);
+  const int tiles = min(s_base, p.max_tiles);
 
   // tile i of the call: its entry without a split
   auto tile_entry = [&](int i) {
@@ -163,77 +171,107 @@ __global__ void __launch_bounds__(kPrefillPlanThreads) prefill_plan_kernel(const
     return e;
   };
 
-  unsigned long long work = 0;
+  PrefillEntry mine;                            // of tile tid, kept for the listing
+  mine.step1 = 0;
   int longest = 0;
   for (int i = tid; i < tiles; i += kPrefillPlanThreads) {
-    const int n = tile_entry(i).step1;
-    work += n;
-    longest = max(longest, n);
+    const PrefillEntry e = tile_entry(i);
+    if (i == tid) mine = e;
+    p.tile_steps[i] = e.step1;
+    longest = max(longest, e.step1);
   }
-  for (int o = 16; o > 0; o >>= 1) {
-    work += __shfl_xor_sync(0xffffffffu, work, o);
-    longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
-  }
-  if (lane == 0) {
-    atomicAdd(&s_work, work);
-    atomicMax(&s_max, longest);
+  for (int o = 16; o > 0; o >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+  if (lane == 0) atomicMax(&s_max, longest);
+  __syncthreads();
+  const int top = s_max;
+
+  // pieces of a tile of n steps under a limit
+  auto pieces_of = [](int n, int limit) { return n > limit ? (n + limit - 1) / limit : 1; };
+  {
+    const int units = max(1, tiles * p.num_kv_heads);
+    const int cut = warp < 16 ? warp + 1 : max(1, (warp - 15) * p.ctas / units);
+    const int limit = p.max_slots > 0 ? max(min(top, kMinSplitSteps), (top + cut - 1) / cut) : max(top, 1);
+    const float big = 0.5f * min(top, limit);
+    float work = 0.f, big_work = 0.f;
+    int bigs = 0, slots = 0, merges = 0;
+    for (int i = lane; i < tiles; i += 32) {
+      const int n = p.tile_steps[i];
+      const int k = pieces_of(n, max(limit, 1));
+      const float each = (k > 1 ? static_cast<float>((n + k - 1) / k) + kPartialSteps : static_cast<float>(n)) + kPieceSteps;
+      work += k * each;
+      if (each > big + kPieceSteps) {
+        bigs += k;
+        big_work += k * each;
+      }
+      if (k > 1) {
+        slots += k;
+        ++merges;
+      }
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+      work += __shfl_xor_sync(0xffffffffu, work, o);
+      big_work += __shfl_xor_sync(0xffffffffu, big_work, o);
+      bigs += __shfl_xor_sync(0xffffffffu, bigs, o);
+      slots += __shfl_xor_sync(0xffffffffu, slots, o);
+      merges += __shfl_xor_sync(0xffffffffu, merges, o);
+    }
+    if (lane == 0) {
+      const float h = static_cast<float>(p.num_kv_heads), c = static_cast<float>(p.ctas);
+      float est = work * h / c;
+      if (bigs > 0) est = fmaxf(est, ceilf(bigs * h / c) * (big_work / bigs));
+      if (merges > 0) est += kMergeSteps;
+      const bool fits = slots <= p.max_slots && merges <= p.max_merges;
+      s_est[warp] = fits || warp == 0 ? est : INFINITY;
+      s_limit[warp] = max(limit, 1);
+    }
   }
   __syncthreads();
-  const long long target = static_cast<long long>(kSplitUnits) * p.ctas;
-  const int limit = max(kMinSplitSteps,
-                        static_cast<int>((static_cast<long long>(s_work) * p.num_kv_heads + target - 1) / target));
-  const int top = s_max;
-  // pieces of a tile of n steps; a tile is left whole when the lists are full
-  auto pieces_of = [&](int n) { return n > limit ? (n + limit - 1) / limit : 1; };
+  int best = 0;                                 // (warp 0's limit is the longest context: no split)
+  for (int w = 1; w < 32; ++w)
+    if (s_est[w] < s_est[best]) best = w;
+  const int limit = s_limit[best];
+
   auto bucket_of = [&](int n) {                 // 0 = longest
     return kPrefillBuckets - 1 -
            (top < kPrefillBuckets ? n : static_cast<int>(static_cast<long long>(n) * (kPrefillBuckets - 1) / top));
   };
-
   for (int pass = 0; pass < 2; ++pass) {
     for (int i = tid; i < tiles; i += kPrefillPlanThreads) {
-      PrefillEntry e = tile_entry(i);
-      const int n = e.step1;
-      const int k = pieces_of(n);
+      const int n = i == tid ? mine.step1 : p.tile_steps[i];
+      const int k = pieces_of(n, limit);
       const int len = (n + k - 1) / k;
       const int bucket = bucket_of(len);
       if (pass == 0) {
         atomicAdd(&s_hist[bucket], k);
         continue;
       }
-      int at = atomicAdd(&s_hist[bucket], k);   // (now the bucket's first index)
+      PrefillEntry e = i == tid ? mine : tile_entry(i);
+      int at = atomicAdd(&s_hist[bucket], k);   // (the bucket's next index)
       int slot = -1;
       if (k > 1) {
-        slot = atomicAdd(&s_slots, k);
-        const int m = atomicAdd(&s_merges, 1);
-        if (m < p.max_merges && slot + k <= p.max_slots)
-          p.merges[m] = PrefillMerge{e.tok0, e.ntok, slot, k};
-        else
-          s_bad = 1;                            // (cannot happen: the lists are sized for the rule above)
+        slot = atomicAdd(&s_slots, k);          // (fits: weighed above)
+        p.merges[atomicAdd(&s_merges, 1)] = PrefillMerge{e.tok0, e.ntok, slot, k};
       }
       for (int j = 0; j < k; ++j, ++at) {
         e.step0 = min(n, j * len);
         e.step1 = min(n, (j + 1) * len);
-        e.slot = k > 1 ? min(slot + j, p.max_slots - 1) : -1;
-        if (at < p.max_entries) p.entries[at] = e;
+        e.slot = k > 1 ? slot + j : -1;
+        p.entries[at] = e;
       }
     }
     __syncthreads();
     if (pass == 0) {
       int total;
-      static_assert(kPrefillBuckets == kPrefillPlanThreads, "one bucket per thread");
       const int own = s_hist[tid];
       const int incl = scan(own, &total);
       s_hist[tid] = incl - own;
-      if (tid == 0) s_base = total;
+      if (tid == 0) p.header->num_entries = total;
       __syncthreads();
     }
   }
   if (tid == 0) {
-    if (s_base > p.max_entries) s_bad = 1;
-    p.header->num_entries = min(s_base, p.max_entries);
-    p.header->num_merges = min(s_merges, p.max_merges);
-    if (s_bad) set_device_error(DEVERR_BAD_LENGTH);
+    p.header->num_merges = s_merges;
+    if (s_bad || s_base > p.max_tiles) set_device_error(DEVERR_BAD_LENGTH);
   }
 }
 
@@ -250,57 +288,67 @@ constexpr int kPrefillMergeWarps = 8;
 
 // out row = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p over the pieces of a
 // split context, in piece order; one warp per row.  Bound by the reads of the
-// partials (mostly in L2, where the attention kernel has just put them).
+// partials (mostly in L2, where the attention kernel has just put them): the
+// weights of 32 pieces are worked out at once, one per lane, and the rows of
+// eight pieces are in flight at a time.
 template <typename T, int D>
 __global__ void __launch_bounds__(kPrefillMergeWarps * 32) prefill_merge_kernel(const PrefillMergeParams p) {
   constexpr int C = D / 32;                     // columns per lane
   const int lane = threadIdx.x & 31;
   allow_dependent_launch();
   wait_prerequisite_grids();
-  const long long total = static_cast<long long>(p.header->num_merges) * p.num_kv_heads * p.rows;
-  const long long step = static_cast<long long>(gridDim.x) * kPrefillMergeWarps;
-  for (long long w = static_cast<long long>(blockIdx.x) * kPrefillMergeWarps + (threadIdx.x >> 5); w < total;
-       w += step) {
-    const int row = static_cast<int>(w % p.rows);
-    const long long mh = w / p.rows;
-    const int h = static_cast<int>(mh % p.num_kv_heads);
-    const PrefillMerge m = p.merges[mh / p.num_kv_heads];
+  const int per = p.num_kv_heads * p.rows;
+  const int total = p.header->num_merges * per;
+  for (int w = blockIdx.x * kPrefillMergeWarps + (threadIdx.x >> 5); w < total; w += gridDim.x * kPrefillMergeWarps) {
+    const int i = w / per, hr = w - i * per;
+    const int h = hr / p.rows, row = hr - h * p.rows;
+    const PrefillMerge m = p.merges[i];
     const int tok = row / p.group;
     if (tok >= m.ntok) continue;
+    const int64_t at0 = (static_cast<int64_t>(m.slot0) * p.num_kv_heads + h) * p.rows + row;
+    const float* acc0 = p.part_acc + at0 * D + lane * C;
     float top = -INFINITY;
-    for (int k = lane; k < m.pieces; k += 32)
-      top = fmaxf(top, p.part_ml[(static_cast<long long>(m.slot0 + k) * p.num_kv_heads + h) * p.rows + row].x);
+    float2 ml = make_float2(-INFINITY, 0.f);
+    for (int k = lane; k < m.pieces; k += 32) {
+      ml = p.part_ml[at0 + static_cast<int64_t>(k) * per];
+      top = fmaxf(top, ml.x);
+    }
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     float acc[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] = 0.f;
     float l = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < m.pieces; ++k) {
-      const long long at = (static_cast<long long>(m.slot0 + k) * p.num_kv_heads + h) * p.rows + row;
-      const float2 ml = p.part_ml[at];
-      if (ml.y == 0.f) continue;                // nothing visible in this piece: no output was written
-      const float f = exp2f(ml.x - top);
+    for (int k0 = 0; k0 < m.pieces; k0 += 32) {
+      const int n = min(32, m.pieces - k0);
+      if (m.pieces > 32) ml = lane < n ? p.part_ml[at0 + static_cast<int64_t>(k0 + lane) * per] : make_float2(0.f, 0.f);
+      // (a piece in which nothing is visible has l = 0, and no output was written)
+      const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - top);
       l += f * ml.y;
-      const float* o = p.part_acc + at * D + lane * C;
-      if constexpr (C == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(o);
-        acc[0] += f * v.x;
-        acc[1] += f * v.y;
-        acc[2] += f * v.z;
-        acc[3] += f * v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(o);
-        acc[0] += f * v.x;
-        acc[1] += f * v.y;
+#pragma unroll 8
+      for (int k = 0; k < n; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, k);
+        const float* o = acc0 + static_cast<int64_t>(k0 + k) * per * D;
+        float v[C];
+        if constexpr (C == 4) {
+          *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(o);
+        } else {
+          *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o);
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[c] += fk == 0.f ? 0.f : fk * v[c];
       }
     }
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     const float inv = l == 0.f ? 0.f : 1.f / l;
     T* dst = static_cast<T*>(p.out) +
-             (static_cast<long long>(m.tok0 + tok) * p.num_kv_heads * p.group + h * p.group + row % p.group) * D +
+             (static_cast<int64_t>(m.tok0 + tok) * p.num_kv_heads * p.group + h * p.group + row % p.group) * D +
              lane * C;
+    T t[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) dst[c] = static_cast<T>(acc[c] * inv);
+    for (int c = 0; c < C; ++c) t[c] = static_cast<T>(acc[c] * inv);
+    if constexpr (sizeof(T) * C == 16) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<uint4*>(t);
+    else if constexpr (sizeof(T) * C == 8) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<uint2*>(t);
+    else *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<uint32_t*>(t);
   }
 }
 

@@ -20,7 +20,10 @@
 //               one box of a 5-D view of the cache that puts the D/64 column
 //               panels of 8 tokens behind one another (1024-byte atoms,
 //               128-byte swizzled), so a tile of 128 tokens is 8 copies for
-//               blocks of 16.
+//               blocks of 16, issued by as many lanes at once.  (One elected
+//               lane issuing them in turn took 1,000 cycles for a tile of 8
+//               beside the softmax warps, against 600 to 800, and held up the
+//               products: 1,300 -> 1,400 us.)
 //   warp 9      issues the MMAs: the whole warp runs the loop and one elected
 //               lane issues, so that the operands stay in uniform registers
 //               (from a single thread's branch a product was issued every 90
@@ -136,24 +139,28 @@ template <int D>
 __host__ __device__ constexpr size_t prefill_umma_smem_bytes() {
   const size_t n = 1024 + 2 * static_cast<size_t>(D / 64) * 128 * 128            // Q tiles
                    + kChunkStages * static_cast<size_t>(D / 64) * 128 * 128      // K/V ring
-                   + 512;                                                        // barriers
+                   + 1024 + 512;                                                 // (m, l) of a row, barriers
   return n < kUmmaMinSmem ? kUmmaMinSmem : n;
 }
 
-// Steps of query tile g of a unit: [step0, end); the limit of its first and last row.
-struct ChunkTile {
-  int end, lim_first, lim_last;
-  bool any;                                      // it has rows
-};
-__device__ __forceinline__ ChunkTile chunk_tile(const PrefillEntry& e, int g, int group, int causal) {
-  ChunkTile c;
+// How the two softmax groups share a unit.  Normally group g has query tile g
+// and every step.  A unit whose rows fit one tile (a chunk of few tokens, a
+// decoding sequence) is dealt by steps instead: both groups hold the same rows,
+// group g takes steps step0 + g, + 2, ..., and group 0 combines the two partial
+// outputs at the end; a lone group would leave half of the softmax warps idle and
+// wait for its own products (48 decoding sequences beside a 512-token chunk,
+// 32/8 heads: 156 -> 137 us; 16 tokens on a 32k context, 64/8 heads: 36 -> 28 us
+// of the kernel).
+__device__ __forceinline__ int chunk_steps(const PrefillEntry& e, int g, int group, int causal) {
   const int per = 128 / group;
-  const int first = g * per, last = min(e.ntok, first + per) - 1;
-  c.any = first < e.ntok;
-  c.lim_first = causal ? min(e.ctx, e.lim0 + first) : e.ctx;
-  c.lim_last = causal ? min(e.ctx, e.lim0 + last) : e.ctx;
-  c.end = c.any ? max(e.step0, min(e.step1, (max(c.lim_last, 0) + kStepTokens - 1) / kStepTokens)) : e.step0;
-  return c;
+  const int last = min(e.ntok, (g + 1) * per) - 1;         // its last token
+  if (last < g * per) return 0;
+  const int lim = causal ? min(e.ctx, e.lim0 + last) : e.ctx;
+  const int end = min(e.step1, (max(lim, 0) + kStepTokens - 1) / kStepTokens);
+  return max(0, end - e.step0);
+}
+__device__ __forceinline__ bool chunk_dual(const PrefillEntry& e, int group, int steps) {
+  return e.ntok * group <= 128 && steps >= 2;
 }
 
 template <typename T, int D>
@@ -174,7 +181,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const uintptr_t base = (reinterpret_cast<uintptr_t>(smem) + 1023) & ~static_cast<uintptr_t>(1023);
   unsigned char* s_q = reinterpret_cast<unsigned char*>(base);          // [tile][panel][128 rows][128 B]
   unsigned char* s_kv = s_q + 2 * kQBytes;                              // [stage][token / 8][panel][8][128 B]
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_kv + NS * static_cast<size_t>(kTileBytes));
+  float2* s_ml = reinterpret_cast<float2*>(s_kv + NS * static_cast<size_t>(kTileBytes));    // [128 rows], dual units
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_ml + 128);
   uint64_t* empty = full + NS;
   uint64_t* grp = empty + NS;
   auto s_full = [&](int g) { return grp + kChunkGroupBars * g; };       // S ready
@@ -186,7 +194,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   uint64_t* q_empty = q_full + 1;
   uint64_t* tail = q_full + 2;
   uint64_t* drain = q_full + 3;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 4);
+  uint64_t* ml_full = q_full + 4;                // group 1's (m, l) of a dual unit
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5;
@@ -210,6 +219,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     mbar_init(q_empty, 1);
     mbar_init(tail, 1);
     mbar_init(drain, 1);
+    mbar_init(ml_full, 4);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -250,19 +260,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (u < 0) continue;
       int h;
       const PrefillEntry en = prefill_unit(prm, u, &h);
-      const ChunkTile c0 = chunk_tile(en, 0, G, prm.causal), c1 = chunk_tile(en, 1, G, prm.causal);
-      const int end = max(c0.end, c1.end);
-      if (end <= en.step0) continue;
+      const int n0 = chunk_steps(en, 0, G, prm.causal), n1 = chunk_steps(en, 1, G, prm.causal);
+      const int steps = max(n0, n1);
+      if (steps == 0) continue;
+      const bool dual = chunk_dual(en, G, steps);
+      const int ahead = dual ? 2 : 1;
       // Q, once the last S of the unit before has completed
       if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (loaded & 1) ^ 1, abort_flag))) {
         ok = false;
         break;
       }
       if (lane == 0) {
-        mbar_arrive_expect_tx(q_full, (c1.any ? 2 : 1) * kQBytes);
-        for (int g = 0; g < (c1.any ? 2 : 1); ++g)
+        const int copies = dual || n1 > 0 ? 2 : 1;
+        mbar_arrive_expect_tx(q_full, copies * kQBytes);
+        for (int g = 0; g < copies; ++g)
           for (int hf = 0; hf < kHalves; ++hf)
-            tma_load_4d(s_q + g * kQBytes + hf * kQPanel, &tm_q, q_full, 0, hf, h * G, en.tok0 + g * (128 / G));
+            tma_load_4d(s_q + g * kQBytes + hf * kQPanel, &tm_q, q_full, 0, hf, h * G, en.tok0 + (dual ? 0 : g * (128 / G)));
       }
       __syncwarp();
       ++loaded;
@@ -279,47 +292,54 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         return (phys * BS + (tok - b * BS)) >> 3;
       };
-      int next = piece_row(en.step0);
-      for (int t = en.step0; ok && t < end; ++t) {
+      // one K or V tile: step t, its pieces' rows in row8 of each lane
+      auto load = [&](bool is_v, int t, int row8) {
         const int ntok = min(kStepTokens, en.ctx - t * kStepTokens);      // >= 1
         const int n = (ntok + piece_rows - 1) / piece_rows;
         const uint32_t tx = static_cast<uint32_t>(n) * (piece_rows / 8) * kAtomRow;
-        const int row8 = next;
-        if (t + 1 < end) next = piece_row(t + 1);
-        for (int kv = 0; kv < 2; ++kv) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1, abort_flag))) {
-            ok = false;
-            break;
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1, abort_flag))) return false;
+        unsigned char* dst = s_kv + static_cast<size_t>(st) * kTileBytes;
+        // the last V tile of a context lands on a barrier of its own first:
+        // the rows behind the context's end are zeroed before it is handed on
+        const bool fix = is_v && ntok < kStepTokens;
+        uint64_t* bar = fix ? tail : &full[st];
+        if (lane == 0) mbar_arrive_expect_tx(bar, tx);
+        __syncwarp();
+        if (lane < n)
+          tma_load_5d(dst + lane * (piece_rows / 8) * kAtomRow, is_v ? &tm_v : &tm_k, bar, 0, 0, 0, row8, h);
+        bool fine = true;
+        if (fix) {
+          // (the copies are in flight whatever happens to the other warps: wait for them alone)
+          fine = __all_sync(0xffffffffu, mbar_wait_drain(tail, tails & 1));
+          ++tails;
+          // 16-byte chunks of rows ntok..127: atom row, panel, row, chunk
+          for (int i = lane; i < (kStepTokens - ntok) * kHalves * 8; i += 32) {
+            const int row = ntok + i / (kHalves * 8), c = i % (kHalves * 8);
+            *reinterpret_cast<uint4*>(dst + (row >> 3) * kAtomRow + (c >> 3) * 1024 + (row & 7) * 128 +
+                                      (c & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
-          unsigned char* dst = s_kv + static_cast<size_t>(st) * kTileBytes;
-          // the last V tile of a context lands on a barrier of its own first:
-          // the rows behind the context's end are zeroed before it is handed on
-          const bool fix = kv == 1 && ntok < kStepTokens;
-          uint64_t* bar = fix ? tail : &full[st];
-          if (lane == 0) mbar_arrive_expect_tx(bar, tx);
+          tc::fence_proxy_async_smem();
           __syncwarp();
-          if (lane < n)
-            tma_load_5d(dst + lane * (piece_rows / 8) * kAtomRow, kv ? &tm_v : &tm_k, bar, 0, 0, 0, row8, h);
-          if (fix) {
-            // (the copies are in flight whatever happens to the other warps: wait for them alone)
-            if (!__all_sync(0xffffffffu, mbar_wait_drain(tail, tails & 1))) ok = false;
-            ++tails;
-            // 16-byte chunks of rows ntok..127: atom row, panel, row, chunk
-            for (int i = lane; i < (kStepTokens - ntok) * kHalves * 8; i += 32) {
-              const int row = ntok + i / (kHalves * 8), c = i % (kHalves * 8);
-              *reinterpret_cast<uint4*>(dst + (row >> 3) * kAtomRow + (c >> 3) * 1024 + (row & 7) * 128 +
-                                        (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[st]);
-          }
-          ++armed;
-          if (++st == NS) {
-            st = 0;
-            ph ^= 1;
-          }
+          if (lane == 0) mbar_arrive(&full[st]);
         }
+        ++armed;
+        if (++st == NS) {
+          st = 0;
+          ph ^= 1;
+        }
+        return fine;
+      };
+      // K of the first `ahead` steps, then V(i), K(i + ahead): the order of their
+      // use; the rows of steps i, i + 1, i + 2 are at hand, read once per step
+      auto rows_at = [&](int i) { return i < steps ? piece_row(en.step0 + i) : 0; };
+      int ra = rows_at(0), rb = rows_at(1), rc = rows_at(2);
+      ok = load(false, en.step0, ra) && (!dual || load(false, en.step0 + 1, rb));
+      for (int i = 0; ok && i < steps; ++i) {
+        const int rv = ra, rk = dual ? rc : rb;
+        ra = rb;
+        rb = rc;
+        rc = rows_at(i + 3);
+        ok = load(true, en.step0 + i, rv) && (i + ahead >= steps || load(false, en.step0 + i + ahead, rk));
       }
     }
     // copies still in flight must land before the CTA may exit
@@ -381,10 +401,48 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         int h;
         const PrefillEntry en = prefill_unit(prm, u, &h);
         int ends[2];
-        ends[0] = chunk_tile(en, 0, G, prm.causal).end;
-        ends[1] = chunk_tile(en, 1, G, prm.causal).end;
+        ends[0] = en.step0 + chunk_steps(en, 0, G, prm.causal);
+        ends[1] = en.step0 + chunk_steps(en, 1, G, prm.causal);
         const int end = max(ends[0], ends[1]);
         if (end <= en.step0) continue;
+        if (chunk_dual(en, G, end - en.step0)) {
+          // the groups take the steps in turn: PV(i), S(i + 2) of group i % 2
+          const int n = end - en.step0;
+          ok = mbar_wait(q_full, loaded & 1, abort_flag);
+          ++loaded;
+          for (int i = -2; ok && i < n; ++i) {
+            const int g = i & 1, vs = st;
+            if (i >= 0) {
+              ok = mbar_wait(&full[vs], ph, abort_flag) && mbar_wait(p_half(g), tiles_g[g] & 1, abort_flag) &&
+                   (i >= 2 || units_g[g] == 0 || mbar_wait(o_free(g), (units_g[g] - 1) & 1, abort_flag));
+              if (!ok) break;
+              advance();
+              tc::fence_after_sync();
+              issue_pv(g, vs, 0, i < 2);
+              ok = mbar_wait(p_full(g), tiles_g[g] & 1, abort_flag);
+              if (!ok) break;
+              ++tiles_g[g];
+              tc::fence_after_sync();
+              issue_pv(g, vs, 1, false);
+            }
+            if (i + 2 < n) {
+              ok = mbar_wait(&full[st], ph, abort_flag);
+              if (!ok) break;
+              tc::fence_after_sync();
+              issue_s(g, st);
+            } else {
+              commit_one(one, o_done(g));
+              ++units_g[g];
+            }
+            if (i >= 0) commit_one(one, &empty[vs]);
+            if (i + 2 < n) {
+              commit_one(one, &empty[st]);
+              advance();
+              if (i + 3 == n) commit_one(one, q_empty);    // the unit's last S was issued
+            }
+          }
+          continue;
+        }
         ok = mbar_wait(q_full, loaded & 1, abort_flag) && mbar_wait(&full[st], ph, abort_flag);
         if (!ok) break;
         ++loaded;
@@ -451,21 +509,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const bool negative = prm.qk_scale < 0.f;
     const float qk = fabsf(prm.qk_scale);
     const bool wide = (reinterpret_cast<uintptr_t>(prm.out) & 31) == 0;
-    int tiles = 0, done = 0;
+    int tiles = 0, done = 0, duals = 0;
     bool ok = true;
     for (int r = 0; ok && r < rounds; ++r) {
       const int u = unit_of(r);
       if (u < 0) continue;
       int h;
       const PrefillEntry en = prefill_unit(prm, u, &h);
-      const ChunkTile ct = chunk_tile(en, g, G, prm.causal);
-      const int tok = (g * 128 + row) / G;                 // token of this row in the unit
+      const int n0 = chunk_steps(en, 0, G, prm.causal), n1 = chunk_steps(en, 1, G, prm.causal);
+      const bool dual = chunk_dual(en, G, max(n0, n1));
+      const int tok0 = dual ? 0 : g * 128 / G;          // first token of this group's rows in the unit
+      const int tok = tok0 + row / G;                      // token of this row
       const int head = row % G;
       const bool valid = tok < en.ntok;
+      const int begin = en.step0 + (dual ? g : 0);
+      const int end = en.step0 + (dual ? max(n0, n1) : g ? n1 : n0);
+      const int stride = dual ? 2 : 1;
+      const int lim_first = prm.causal ? min(en.ctx, en.lim0 + tok0) : en.ctx;
       const int lim = prm.causal ? min(en.ctx, en.lim0 + min(tok, en.ntok - 1)) : en.ctx;
       float m = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
-      for (int t = en.step0; t < ct.end; ++t, ++tiles) {
+      for (int t = begin; t < end; t += stride, ++tiles) {
         if (!__all_sync(0xffffffffu, mbar_wait(s_full(g), tiles & 1, abort_flag))) {
           ok = false;
           break;
@@ -482,7 +546,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           for (int j = 0; j < 128; ++j) x[j] ^= 0x80000000u;
         }
         const int nv = lim - t * kStepTokens;              // tokens of this step the row sees
-        const bool masked = ct.lim_first < (t + 1) * kStepTokens;       // uniform over the tile
+        const bool masked = lim_first < (t + 1) * kStepTokens;       // uniform over the tile
         float mul = qk;
         if (masked) {
           mul = 1.f;                                       // scaled here: 0 * inf must not reach the weights
@@ -502,7 +566,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (__any_sync(0xffffffffu, c > m + kTau)) {
           const float mn = c > m + kTau ? c : m;
           const float f = mn != m ? exp2_approx(m - mn) : 1.f;     // 0 when m was -inf
-          if (t > en.step0) {
+          if (t > begin) {
 #pragma unroll 1
             for (int ob = 0; ob < D / 16; ++ob) {
               uint32_t o[16];
@@ -569,8 +633,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         fadd2(l2, ls[1]);
       }
       if (!ok) break;
-      const float l = l2.x + l2.y;
-      const bool have = ct.end > en.step0;                 // O holds this unit's product
+      float l = l2.x + l2.y;
+      const bool have = end > begin;                       // O holds this unit's product
       if (have) {
         if (!__all_sync(0xffffffffu, mbar_wait(o_done(g), done & 1, abort_flag))) {
           ok = false;
@@ -579,54 +643,78 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         ++done;
         tc::fence_after_sync();
       }
-      if (en.slot >= 0) {
-        const int64_t at = (static_cast<int64_t>(en.slot) * prm.num_kv_heads + h) * kPrefillRows16 + g * 128 + row;
-        if (valid) prm.part_ml[at] = make_float2(m, l);
+      float f0 = 1.f, f1 = 0.f;                            // weights of the two groups' outputs
+      if (dual) {
+        if (g == 1) {
+          s_ml[row] = make_float2(m, l);
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ml_full);
+          continue;                                        // (group 0 reads both and frees both)
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(ml_full, duals & 1, abort_flag))) {
+          ok = false;
+          break;
+        }
+        ++duals;
+        tc::fence_after_sync();
+        const float2 other = s_ml[row];
+        const float top = fmaxf(m, other.x);
+        f0 = l == 0.f ? 0.f : exp2_approx(m - top);
+        f1 = other.y == 0.f ? 0.f : exp2_approx(other.x - top);
+        l = f0 * l + f1 * other.y;
+        m = top;
+      }
+      const int64_t at = (static_cast<int64_t>(en.slot) * prm.num_kv_heads + h) * kPrefillRows16 +
+                         (dual ? 0 : g * 128) + row;
+      T* dst = static_cast<T*>(prm.out) +
+               (static_cast<int64_t>(en.tok0 + tok) * prm.num_kv_heads * G + h * G + head) * D;
+      const float inv = l == 0.f ? 0.f : 1.f / l;          // a row that sees nothing is zero
+      if (en.slot >= 0 && valid) prm.part_ml[at] = make_float2(m, l);
+#pragma unroll 1
+      for (int cb = 0; cb < D / 32; ++cb) {
+        uint32_t o[32];
         if (have) {
-#pragma unroll
-          for (int cb = 0; cb < D / 32; ++cb) {
-            uint32_t o[32];
-            tc::tmem_ld32(o_col + cb * 32, o);
+          tc::tmem_ld32(o_col + cb * 32, o);
+          tc::tmem_wait_ld();
+          if (dual) {
+            uint32_t o1[32];
+            tc::tmem_ld32(o_col + kUmmaGroupCols + cb * 32, o1);
             tc::tmem_wait_ld();
-            if (valid) {
 #pragma unroll
-              for (int j = 0; j < 32; j += 8) {
-                const uint32_t w[8] = {o[j], o[j + 1], o[j + 2], o[j + 3], o[j + 4], o[j + 5], o[j + 6], o[j + 7]};
-                store32(prm.part_acc + at * D + cb * 32 + j, w, true);
-              }
-            }
+            for (int j = 0; j < 32; ++j)
+              o[j] = __float_as_uint(f0 * __uint_as_float(o[j]) + f1 * __uint_as_float(o1[j]));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = 0u;
+        }
+        // (no divergence past this iteration: the tensor-memory loads take the whole warp)
+        if (valid && en.slot >= 0) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            const uint32_t w[8] = {o[j], o[j + 1], o[j + 2], o[j + 3], o[j + 4], o[j + 5], o[j + 6], o[j + 7]};
+            store32(prm.part_acc + at * D + cb * 32 + j, w, true);
+          }
+        } else if (valid) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              w[i] = M::pack(__uint_as_float(o[j + 2 * i]) * inv, __uint_as_float(o[j + 2 * i + 1]) * inv);
+            store32(dst + cb * 32 + j, w, wide);
           }
         }
-      } else {
-        T* dst = static_cast<T*>(prm.out) +
-                 (static_cast<int64_t>(en.tok0 + tok) * prm.num_kv_heads * G + h * G + head) * D;
-        const float inv = l == 0.f ? 0.f : 1.f / l;        // a row that sees nothing is zero
-#pragma unroll
-        for (int cb = 0; cb < D / 32; ++cb) {
-          uint32_t o[32];
-          if (have) {
-            tc::tmem_ld32(o_col + cb * 32, o);
-            tc::tmem_wait_ld();
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = 0u;
-          }
-          if (valid) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 16) {
-              uint32_t w[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                w[i] = M::pack(__uint_as_float(o[j + 2 * i]) * inv, __uint_as_float(o[j + 2 * i + 1]) * inv);
-              store32(dst + cb * 32 + j, w, wide);
-            }
-          }
-        }
+        __syncwarp();
       }
       if (have) {
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(o_free(g));
+        if (lane == 0) {
+          mbar_arrive(o_free(g));
+          if (dual) mbar_arrive(o_free(1));
+        }
       }
     }
   }

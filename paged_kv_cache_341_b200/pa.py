@@ -342,26 +342,39 @@ def pa_update_block_tables(block_tables, updates, context_lens=None, new_lens=No
                                        _dev(new_lens, "new_lens", torch.int32) if nl else None, nl, _stream(stream)))
 
 
-def _on_current_device(tensors):
-    """The calls launch on the current device: refuse tensors of another one."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != cur:
-            raise ValueError("tensor on %s, but the current device is cuda:%d" % (t.device, cur))
-
-
-def _token_rows(t, name, dtype, shape):
-    """Pointer and token stride of a [T, H, D] CUDA tensor whose rows [H, D] are contiguous."""
+def _refuse(t, name, dtype, device):
     if not (isinstance(t, torch.Tensor) and t.is_cuda):
         raise TypeError("%s must be a CUDA tensor" % name)
     if t.dtype != dtype:
         raise TypeError("%s must have dtype %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    row = shape[1] * shape[2]
-    if t.shape[0] and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != shape[2])):
+    if t.get_device() != device:
+        raise ValueError("%s is on %s, but the current device is cuda:%d" % (name, t.device, device))
+    raise ValueError("%s must be contiguous" % name)
+
+
+def _ptr(t, name, dtype, device):
+    """Address of a contiguous tensor of ``dtype`` on the current device (an int; the short form of ``_dev``)."""
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        _refuse(t, name, dtype, device)
+    return t.data_ptr()
+
+
+def _raw_stream(stream, device):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _token_rows(t, name, dtype, device, heads, dim):
+    """Address and token stride of a [T, heads, dim] tensor whose token rows are contiguous."""
+    if t.dtype is not dtype or t.get_device() != device:
+        _refuse(t, name, dtype, device)
+    if t.is_contiguous():
+        return t.data_ptr(), heads * dim
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != dim):
         raise ValueError("%s must have contiguous token rows" % name)
-    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else row
+    return t.data_ptr(), st[0] if t.shape[0] > 1 else heads * dim
 
 
 def pa_rope_append(q, k_new, v_new, positions, inv_freq, slot_mapping, k_cache, v_cache, q_out, pair_axis=None,
@@ -372,62 +385,67 @@ def pa_rope_append(q, k_new, v_new, positions, inv_freq, slot_mapping, k_cache, 
     float32 [rotary_dim / 2]; slot_mapping int64 [T]; pair_axis int32 [rotary_dim / 2] (None: axis 0);
     caches [NB, bs, Hkv, D]; q_out [T, Hq, D] (may be q).
     """
-    nb, bs, hkv, d = k_cache.shape
+    nb, bs, hkv, d = shape = k_cache.shape
     dt = k_cache.dtype
-    t, hq = q.shape[0], q.shape[1]
-    if tuple(v_cache.shape) != tuple(k_cache.shape) or tuple(q_out.shape) != (t, hq, d):
+    qshape = q.shape
+    t, hq = qshape[0], qshape[1]
+    kv = (t, hkv, d)
+    if v_cache.shape != shape or q_out.shape != qshape or qshape != (t, hq, d):
         raise ValueError("shape mismatch between q, q_out and caches")
+    if k_new.shape != kv or v_new.shape != kv:
+        raise ValueError("k_new and v_new must be [T, Hkv, D]")
     axes = 1 if positions.dim() == 1 else positions.shape[0]
+    half = inv_freq.numel()
     if positions.numel() != axes * t or slot_mapping.numel() != t:
         raise ValueError("positions must be [axes, T] and slot_mapping [T]")
-    if pair_axis is not None and pair_axis.numel() != inv_freq.numel():
+    if pair_axis is not None and pair_axis.numel() != half:
         raise ValueError("pair_axis must have one entry per pair of inv_freq")
-    qp, qs = _token_rows(q, "q", dt, (t, hq, d))
-    kp, ks = _token_rows(k_new, "k_new", dt, (t, hkv, d))
-    vp, vs = _token_rows(v_new, "v_new", dt, (t, hkv, d))
-    _on_current_device((q, k_new, v_new, positions, inv_freq, pair_axis, slot_mapping, k_cache, v_cache, q_out))
-    _check(_lib.pa_rope_append(qp, qs, kp, ks, vp, vs, _dev(positions, "positions", torch.int32), axes,
-                               _dev(inv_freq, "inv_freq", torch.float32),
-                               None if pair_axis is None else _dev(pair_axis, "pair_axis", torch.int32),
-                               2 * inv_freq.numel(), 1 if interleaved else 0,
-                               _dev(slot_mapping, "slot_mapping", torch.int64), t, _dev(q_out, "q_out", dt),
-                               _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache", dt), nb, bs, hq, hkv, d,
-                               DTYPE_CODE[dt], _stream(stream)))
+    dev = torch.cuda.current_device() if q.is_cuda else -2
+    qp, qs = _token_rows(q, "q", dt, dev, hq, d)
+    kp, ks = _token_rows(k_new, "k_new", dt, dev, hkv, d)
+    vp, vs = _token_rows(v_new, "v_new", dt, dev, hkv, d)
+    _check(_lib.pa_rope_append(qp, qs, kp, ks, vp, vs, _ptr(positions, "positions", torch.int32, dev), axes,
+                               _ptr(inv_freq, "inv_freq", torch.float32, dev),
+                               None if pair_axis is None else _ptr(pair_axis, "pair_axis", torch.int32, dev),
+                               2 * half, 1 if interleaved else 0,
+                               _ptr(slot_mapping, "slot_mapping", torch.int64, dev), t,
+                               _ptr(q_out, "q_out", dt, dev), _ptr(k_cache, "k_cache", dt, dev),
+                               _ptr(v_cache, "v_cache", dt, dev), nb, bs, hq, hkv, d, DTYPE_CODE[dt],
+                               _raw_stream(stream, dev)))
 
 
 def pa_move_blocks(k_caches, v_caches, moves, block_tables=None, stream=None):
     """Run a compaction's moves on every layer's cache and rewrite the device block tables.
 
-    k_caches/v_caches: lists of [NB, bs, Hkv, D] CUDA tensors, one per layer; moves: int32 CUDA [M, 2] of
+    k_caches/v_caches: sequences of [NB, bs, Hkv, D] CUDA tensors, one per layer; moves: int32 CUDA [M, 2] of
     (source, destination), sources increasing; block_tables: int32 CUDA [rows, cols] with unit column stride.
     """
-    k_caches, v_caches = list(k_caches), list(v_caches)
-    if not k_caches or len(k_caches) != len(v_caches):
+    n = len(k_caches)
+    if n == 0 or len(v_caches) != n:
         raise ValueError("need as many K caches as V caches, at least one")
     shape, dt = k_caches[0].shape, k_caches[0].dtype
-    if len({c.data_ptr() for c in k_caches + v_caches}) != 2 * len(k_caches):
+    if len({c.data_ptr() for caches in (k_caches, v_caches) for c in caches}) != 2 * n:
         raise ValueError("the caches must be distinct")
-    ptrs = []
-    for c in k_caches + v_caches:
-        if c.shape != shape:
-            raise ValueError("all caches must have the shape of the first")
-        ptrs.append(_dev(c, "cache", dt).value)
-    n = len(k_caches)
-    kp, vp = (_vp * n)(*ptrs[:n]), (_vp * n)(*ptrs[n:])
+    dev = torch.cuda.current_device() if k_caches[0].is_cuda else -2
+    kp, vp = (_vp * n)(), (_vp * n)()
+    for caches, ptrs in ((k_caches, kp), (v_caches, vp)):
+        for i, c in enumerate(caches):
+            if c.shape != shape:
+                raise ValueError("all caches must have the shape of the first")
+            ptrs[i] = _ptr(c, "cache", dt, dev)
     rows = cols = stride = 0
     tp = None
     if block_tables is not None and block_tables.numel():
         if block_tables.dim() != 2 or block_tables.stride(1) != 1:
             raise ValueError("block_tables must be a 2-D tensor with unit column stride")
-        if block_tables.dtype != torch.int32 or not block_tables.is_cuda:
-            raise TypeError("block_tables must be an int32 CUDA tensor")
+        if block_tables.dtype is not torch.int32 or block_tables.get_device() != dev:
+            _refuse(block_tables, "block_tables", torch.int32, dev)
         rows, cols = block_tables.shape
         stride = max(block_tables.stride(0), cols)
-        tp = ctypes.c_void_p(block_tables.data_ptr())
-    _on_current_device(k_caches + v_caches + [moves, block_tables])
+        tp = block_tables.data_ptr()
     nb, bs, hkv, d = shape
-    _check(_lib.pa_move_blocks(kp, vp, n, _dev(moves, "moves", torch.int32), moves.numel() // 2, nb, bs, hkv, d, tp,
-                               rows, cols, stride, DTYPE_CODE[dt], _stream(stream)))
+    _check(_lib.pa_move_blocks(kp, vp, n, _ptr(moves, "moves", torch.int32, dev), moves.numel() // 2, nb, bs, hkv, d,
+                               tp, rows, cols, stride, DTYPE_CODE[dt], _raw_stream(stream, dev)))
 
 
 def pa_prefill_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
@@ -452,30 +470,31 @@ def pa_prefill_attention(q, k_cache, v_cache, block_tables, context_lens, q_star
     context_lens int32 [S] (with causal, including the chunk itself).  The workspace
     (pa_prefill_workspace_size bytes) is allocated here through torch when not given.
     """
-    t, hq, d = q.shape
-    nb, bs, hkv, d2 = k_cache.shape
-    if d2 != d or tuple(out.shape) != (t, hq, d) or tuple(v_cache.shape) != tuple(k_cache.shape):
+    t, hq, d = qshape = q.shape
+    nb, bs, hkv, d2 = shape = k_cache.shape
+    if d2 != d or out.shape != qshape or v_cache.shape != shape:
         raise ValueError("shape mismatch between q, caches and out")
     if block_tables.dim() != 2:
         raise ValueError("block_tables must be [S, max_blocks]")
     s, mb = block_tables.shape
     if context_lens.numel() != s or q_starts.numel() != s + 1:
         raise ValueError("context_lens must be [S] and q_starts [S + 1]")
-    code = DTYPE_CODE[k_cache.dtype]
-    qp, op = _dev(q, "q", k_cache.dtype), _dev(out, "out", k_cache.dtype)
-    _on_current_device((q, k_cache, v_cache, block_tables, context_lens, q_starts, out, workspace))
+    dt = k_cache.dtype
+    dev = torch.cuda.current_device() if q.is_cuda else -2
+    qp, op = _ptr(q, "q", dt, dev), _ptr(out, "out", dt, dev)
     if workspace is None:
         # (on the stream that uses it, so that the allocator orders its reuse)
         if stream is not None and not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream))
         with torch.cuda.stream(stream):
             workspace = prefill_workspace(t, s, hq, hkv, d, mb, bs, device=q.device) if t and s else q
-    _check(_lib.pa_prefill_attention(qp, _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache", k_cache.dtype), nb,
-                                     _dev(block_tables, "block_tables", torch.int32), mb,
-                                     _dev(context_lens, "context_lens", torch.int32),
-                                     _dev(q_starts, "q_starts", torch.int32), t, s, hq, hkv, d, bs, float(scale),
-                                     1 if causal else 0, _dev(workspace, "workspace"),
-                                     workspace.numel() * workspace.element_size(), op, code, _stream(stream)))
+    _check(_lib.pa_prefill_attention(qp, _ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev), nb,
+                                     _ptr(block_tables, "block_tables", torch.int32, dev), mb,
+                                     _ptr(context_lens, "context_lens", torch.int32, dev),
+                                     _ptr(q_starts, "q_starts", torch.int32, dev), t, s, hq, hkv, d, bs, scale,
+                                     1 if causal else 0, _ptr(workspace, "workspace", workspace.dtype, dev),
+                                     workspace.numel() * workspace.element_size(), op, DTYPE_CODE[dt],
+                                     _raw_stream(stream, dev)))
 
 
 def pa_read_stream(buf, sink, stream=None):
