@@ -40,8 +40,7 @@ struct PrefillArgs {
 constexpr int kPrefillMaxCtas = 148;
 
 // Workspace: [header 256 B][tile ends][tile steps][entries][merges][partial (m, l)][partial outputs].
-// There is room for kSplitUnits pieces of split contexts per CTA (over all
-// heads); the planner leaves contexts whole rather than take more.
+// There is room for kSplitUnits pieces of 256 rows per CTA (over all heads); the planner leaves contexts whole rather than take more.
 struct PrefillLayout {
   size_t ends, steps, entries, merges, ml, acc, total;
   int max_tiles, max_entries, max_merges, max_slots;
@@ -52,8 +51,10 @@ PrefillLayout prefill_layout(long long T, long long S, long long Hq, long long H
   const long long G = Hq / Hkv;
   const long long tiles = std::min(T, S) + T * G / rows;                  // every non-empty chunk may end in a part tile
   const long long steps = (cap + pa::kStepTokens - 1) / pa::kStepTokens;
-  const long long pieces = std::min(static_cast<long long>(pa::kSplitUnits) * kPrefillMaxCtas / Hkv, tiles * steps);
-  const bool split = steps > pa::kMinSplitSteps && pieces >= 2;
+  const long long room = static_cast<long long>(pa::kSplitUnits) * kPrefillMaxCtas * (pa::kPrefillRows16 / rows);
+  const long long pieces = std::min(room / Hkv, tiles * steps);
+  const pa::PlanCost& cost = rows == pa::kPrefillRows16 ? pa::kPlanCost16 : pa::kPlanCost32;
+  const bool split = steps > cost.min_steps && pieces >= 2;
   PrefillLayout L;
   L.max_tiles = static_cast<int>(tiles);
   L.max_slots = split ? static_cast<int>(pieces) : 0;
@@ -151,6 +152,7 @@ pa_status launch_prefill(const PrefillArgs& a) {
   pp.cap = a.max_blocks * a.BS;
   pp.ctas = std::min(dev.sms, kPrefillMaxCtas);
   pp.max_tiles = L.max_tiles;
+  pp.cost = kTensor ? pa::kPlanCost16 : pa::kPlanCost32;
   pp.tile_steps = reinterpret_cast<int*>(ws + L.steps);
   pp.max_merges = L.max_merges;
   pp.max_slots = L.max_slots;
@@ -185,11 +187,11 @@ pa_status launch_prefill(const PrefillArgs& a) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(prefill f32)");
     int per_sm = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, 256, smem);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, pa::kPrefillThreads32, smem);
     if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor(prefill f32)");
     if (per_sm < 1) return pa::fail(PA_ERR_UNSUPPORTED, "pa_prefill_attention: kernel does not fit on an SM");
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(units, static_cast<long long>(per_sm) * dev.sms)));
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(pa::kPrefillThreads32);
     cfg.dynamicSmemBytes = smem;
     e = cudaLaunchKernelEx(&cfg, kern, prm);
     if (e != cudaSuccess) return cuda_fail(e, "prefill_f32_kernel launch");

@@ -5,13 +5,16 @@
 // tokens j < lim(t), one pass over the context with a running maximum and sum
 // per row in float32.
 //
-// One CTA of 16 x 16 threads takes one unit (prefill_plan.cuh): 64 query rows
-// of a KV head and a range of its context, 64 tokens at a time.  Q, K, V and
-// the weights P are float32 in shared memory; each thread holds a 4 x 4 piece
-// of S = Q K^T (rows 4 ty.., columns tx + 16 j: neighbouring threads read
-// neighbouring K rows, whose stride of D + 4 floats keeps 16-byte reads free
-// of bank conflicts) and a 4 x D/16 piece of O.  Bound by the FMA pipe and the
-// shared-memory reads that feed it.
+// One CTA of 16 x 8 threads takes one unit (prefill_plan.cuh): 32 query rows of
+// a KV head and a range of its context, 32 tokens at a time.  Q, K, V and the
+// weights P are float32 in shared memory; each thread holds a 4 x 2 piece of
+// S = Q K^T (rows 4 ty.., columns tx + 16 j: neighbouring threads read
+// neighbouring K rows, whose stride of D + 4 floats keeps 16-byte reads free of
+// bank conflicts) and a 4 x D/16 piece of O; the next tile's K and V wait in
+// registers.  Bound by the FMA pipe and the shared-memory reads that feed it.
+// Small tiles, several CTAs per SM: tiles of 64 rows x 64 tokens with 256
+// threads took 10 us each for a handful of rows (4 sequences of up to 45 tokens
+// on 300, head_dim 64: 43 us; see the measured table for this form).
 #ifndef PAGEDATTN_PREFILL_CUH
 #define PAGEDATTN_PREFILL_CUH
 
@@ -57,18 +60,21 @@ __device__ __forceinline__ long long prefill_snake(int r, int b, int g) {
   return static_cast<long long>(r) * g + (r & 1 ? g - 1 - b : b);
 }
 
-constexpr int kPrefillTile32 = 64;               // context tokens per tile
+constexpr int kPrefillTile32 = 32;               // context tokens per tile
+constexpr int kPrefillThreads32 = 4 * kPrefillRows32;
 
 template <int D>
 __host__ __device__ constexpr size_t prefill_f32_smem_bytes() {
-  return sizeof(float) * (2 * 64 * (D + 4) + 64 * D + 64 * (64 + 4));
+  return sizeof(float) * (kPrefillRows32 * (D + 4) + kPrefillTile32 * (2 * D + 4) + kPrefillRows32 * (kPrefillTile32 + 4));
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(256) prefill_f32_kernel(const PrefillParams prm) {
-  constexpr int R = kPrefillRows32, N = kPrefillTile32, LD = D + 4, LP = N + 4;
+__global__ void __launch_bounds__(kPrefillThreads32) prefill_f32_kernel(const PrefillParams prm) {
+  constexpr int R = kPrefillRows32, N = kPrefillTile32, LD = D + 4, LP = N + 4, NT = kPrefillThreads32;
+  constexpr int J = N / 16;                      // columns of S per thread
   constexpr int E = Chunk<T>::kElems;
   constexpr int CPR = D / E;                     // 16-byte chunks per row
+  constexpr int NC = N * CPR / NT;              // chunks of K (and of V) per thread and tile
   constexpr int OC = D / 64;                     // float4 output pieces per thread and row
   extern __shared__ __align__(16) float smem_f[];
   float* s_q = smem_f;
@@ -100,7 +106,7 @@ __global__ void __launch_bounds__(256) prefill_f32_kernel(const PrefillParams pr
     const int32_t* table = prm.block_tables + static_cast<int64_t>(en.seq) * prm.max_blocks;
     const int rows = en.ntok * G;
     __syncthreads();                             // the previous unit's readers of shared memory
-    for (int i = tid; i < R * CPR; i += 256) {
+    for (int i = tid; i < R * CPR; i += NT) {
       const int r = i / CPR, c = i % CPR;
       float x[E];
 #pragma unroll
@@ -126,55 +132,72 @@ __global__ void __launch_bounds__(256) prefill_f32_kernel(const PrefillParams pr
     }
     const int tok_lo = en.step0 * kStepTokens;
     const int tok_hi = min(en.ctx, en.step1 * kStepTokens);
+    // the next tile's chunks, read into registers while this one is worked on:
+    // first the blocks, then K and V, all in flight together
+    uint4 rk[NC], rv[NC];
+    auto fetch = [&](int t0) {
+      int64_t at[NC];
+#pragma unroll
+      for (int k = 0; k < NC; ++k) {
+        const int i = tid + NT * k, r = i / CPR, c = i % CPR, tok = t0 + r;
+        at[k] = -1;
+        if (tok < tok_hi) {
+          const int b = tok / BS, phys = table[b];
+          if (phys < 0 || phys >= prm.num_blocks)
+            set_device_error(DEVERR_BAD_BLOCK_ID);
+          else
+            at[k] = ((static_cast<int64_t>(phys) * BS + (tok - b * BS)) * Hkv + h) * D + c * E;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < NC; ++k) {
+        rk[k] = rv[k] = make_uint4(0, 0, 0, 0);
+        if (at[k] >= 0) {
+          rk[k] = *reinterpret_cast<const uint4*>(static_cast<const T*>(prm.k_cache) + at[k]);
+          rv[k] = *reinterpret_cast<const uint4*>(static_cast<const T*>(prm.v_cache) + at[k]);
+        }
+      }
+    };
+    if (tok_lo < tok_hi) fetch(tok_lo);
     for (int t0 = tok_lo; t0 < tok_hi; t0 += N) {
       __syncthreads();
-      for (int i = tid; i < N * CPR; i += 256) {
-        const int r = i / CPR, c = i % CPR;
-        float k[E], v[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) k[e] = v[e] = 0.f;
-        const int tok = t0 + r;
-        if (tok < tok_hi) {
-          const int b = tok / BS;
-          const int phys = table[b];
-          if (phys < 0 || phys >= prm.num_blocks) {
-            set_device_error(DEVERR_BAD_BLOCK_ID);
-          } else {
-            const int64_t at = ((static_cast<int64_t>(phys) * BS + (tok - b * BS)) * Hkv + h) * D + c * E;
-            widen(static_cast<const T*>(prm.k_cache) + at, k);
-            widen(static_cast<const T*>(prm.v_cache) + at, v);
-          }
-        }
+      for (int k = 0; k < NC; ++k) {
+        const int i = tid + NT * k, r = i / CPR, c = i % CPR;
+        float x[E], y[E];
+        widen(&rk[k], x);
+        widen(&rv[k], y);
 #pragma unroll
         for (int e = 0; e < E; e += 4) {
-          *reinterpret_cast<float4*>(s_k + r * LD + c * E + e) = make_float4(k[e], k[e + 1], k[e + 2], k[e + 3]);
-          *reinterpret_cast<float4*>(s_v + r * D + c * E + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          *reinterpret_cast<float4*>(s_k + r * LD + c * E + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+          *reinterpret_cast<float4*>(s_v + r * D + c * E + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
         }
       }
       __syncthreads();
-      float s[4][4];
+      if (t0 + N < tok_hi) fetch(t0 + N);
+      float s[4][J];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+        for (int j = 0; j < J; ++j) s[i][j] = 0.f;
 #pragma unroll 4
       for (int d = 0; d < D; d += 4) {
-        float4 a[4], b[4];
+        float4 a[4], b[J];
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(s_q + (4 * ty + i) * LD + d);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(s_k + (tx + 16 * j) * LD + d);
+        for (int j = 0; j < J; ++j) b[j] = *reinterpret_cast<const float4*>(s_k + (tx + 16 * j) * LD + d);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < J; ++j)
             s[i][j] = fmaf(a[i].w, b[j].w, fmaf(a[i].z, b[j].z, fmaf(a[i].y, b[j].y, fmaf(a[i].x, b[j].x, s[i][j]))));
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float c = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < J; ++j) {
           s[i][j] = t0 + tx + 16 * j < lim[i] ? s[i][j] * prm.qk_scale : -INFINITY;
           c = fmaxf(c, s[i][j]);
         }
@@ -193,13 +216,13 @@ __global__ void __launch_bounds__(256) prefill_f32_kernel(const PrefillParams pr
           o[i][k].w *= f;
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < J; ++j) {
           const float w = exp2f(s[i][j] - mu);
           l[i] += w;
           s_p[(4 * ty + i) * LP + tx + 16 * j] = w;
         }
       }
-      __syncthreads();
+      __syncwarp();                              // (a row of P is written and read by the same warp)
 #pragma unroll 2
       for (int j = 0; j < N; j += 4) {
         float4 w[4];

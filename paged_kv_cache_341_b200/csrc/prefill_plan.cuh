@@ -20,9 +20,8 @@ namespace pa {
 
 constexpr int kStepTokens = 128;               // context tokens per K/V step
 constexpr int kPrefillRows16 = 256;            // rows per tile, 16-bit caches (two MMA tiles of 128)
-constexpr int kPrefillRows32 = 64;             // rows per tile, float32 caches
-constexpr int kMinSplitSteps = 2;              // a piece of a split context is at least about this long
-constexpr int kSplitUnits = 2;                 // pieces of split contexts per CTA that the workspace has room for
+constexpr int kPrefillRows32 = 32;             // rows per tile, float32 caches
+constexpr int kSplitUnits = 2;                 // pieces of 256 rows per CTA that the workspace has room for
 constexpr int kPrefillPlanThreads = 1024;
 constexpr int kPrefillBuckets = 1024;
 
@@ -45,6 +44,20 @@ struct PrefillHeader {
   int num_entries, num_merges;
 };
 
+// How long the attention kernel takes for a work list, in K/V steps, from sums
+// over its pieces: every piece costs its steps and `piece` for its start and
+// end, a piece of a split context also `partial` for its partial result; C
+// CTAs take the pieces longest first, so that no schedule beats the average,
+// and pieces of more than half of the longest share no CTA unless they fill
+// more than one round; a split call pays `merge` for the merge.
+struct PlanCost {
+  int min_steps;                 // a piece of a split context is at least about this long
+  float piece, partial, merge;   // in steps, as above
+};
+// (a step takes about 1.5 us with tensor cores, and 4 to 8 us without)
+constexpr PlanCost kPlanCost16{2, 2.f, 1.5f, 3.f};
+constexpr PlanCost kPlanCost32{1, 0.5f, 0.2f, 0.7f};
+
 struct PrefillPlanParams {
   const int32_t* q_starts;       // [S + 1]
   const int32_t* context_lens;   // [S]
@@ -57,6 +70,7 @@ struct PrefillPlanParams {
   int ctas;                      // CTAs of the attention grid
   int max_tiles, max_merges, max_slots;        // capacities; slots are per KV head
   int* tile_steps;               // [max_tiles]
+  PlanCost cost;
 };
 
 // Chunk of sequence s, clamped into the arrays: tokens [lo, lo + n), context.
@@ -67,16 +81,6 @@ __device__ __forceinline__ void prefill_seq(const PrefillPlanParams& p, int s, i
   *ctx = min(max(c, 0), p.cap);
   *bad = *lo != a || *lo + *n != b || *ctx != c;
 }
-
-// How long the attention kernel takes for a work list, in K/V steps, from sums
-// over its pieces: every piece costs its steps and kPieceSteps for its start
-// and end, a piece of a split context also kPartialSteps for its partial; C
-// CTAs take the pieces longest first, so that no schedule beats the average,
-// and pieces of more than half of the longest share no CTA unless they fill
-// more than one round; a split call pays kMergeSteps for the merge.
-constexpr float kPieceSteps = 2.f;
-constexpr float kPartialSteps = 1.5f;
-constexpr float kMergeSteps = 3.f;
 
 // One CTA lists the work of a call, longest pieces first (a counting sort on
 // their steps), and decides where contexts are split: 32 limits on the steps of
@@ -93,6 +97,9 @@ __global__ void __launch_bounds__(kPrefillPlanThreads) prefill_plan_kernel(const
   __shared__ float s_est[32];
   __shared__ int s_limit[32];
   __shared__ int s_base, s_max, s_slots, s_merges, s_bad;
+  // of up to kPrefillPlanThreads sequences and tiles, kept here (else in the workspace)
+  __shared__ int s_end[kPrefillPlanThreads], s_steps[kPrefillPlanThreads];
+  __shared__ int4 s_seq[kPrefillPlanThreads];   // first token, tokens, context
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   allow_dependent_launch();
   if (tid == 0) s_base = s_max = s_slots = s_merges = s_bad = 0;
@@ -123,6 +130,9 @@ __global__ void __launch_bounds__(kPrefillPlanThreads) prefill_plan_kernel(const
     return r;
   };
 
+  const bool near_seqs = p.num_seqs <= kPrefillPlanThreads;
+  const int* ends = near_seqs ? s_end : p.tile_ends;
+
   // tiles of sequences 0 .. s
   for (int s0 = 0; s0 < p.num_seqs; s0 += kPrefillPlanThreads) {
     const int s = s0 + tid;
@@ -133,29 +143,37 @@ __global__ void __launch_bounds__(kPrefillPlanThreads) prefill_plan_kernel(const
       prefill_seq(p, s, &lo, &n, &ctx, &bad);
       if (bad) s_bad = 1;
       tiles = static_cast<int>((static_cast<long long>(n) * p.group + p.rows - 1) / p.rows);
+      if (near_seqs) s_seq[s] = make_int4(lo, n, ctx, 0);
     }
     int total;
     const int before = s_base;
     const int incl = scan(tiles, &total) + before;
-    if (s < p.num_seqs) p.tile_ends[s] = incl;
+    if (s < p.num_seqs) (near_seqs ? s_end : p.tile_ends)[s] = incl;
     if (tid == 0) s_base = before + total;
     __syncthreads();
   }
   // disjoint chunks fill the list exactly; overlapping ones (an error) are cut off
   const int tiles = min(s_base, p.max_tiles);
+  int* steps = tiles <= kPrefillPlanThreads ? s_steps : p.tile_steps;
 
   // tile i of the call: its entry without a split
   auto tile_entry = [&](int i) {
     int lo_s = 0, hi_s = p.num_seqs - 1;
     while (lo_s < hi_s) {
       const int mid = (lo_s + hi_s) >> 1;
-      if (p.tile_ends[mid] <= i) lo_s = mid + 1;
+      if (ends[mid] <= i) lo_s = mid + 1;
       else hi_s = mid;
     }
-    const int first = lo_s > 0 ? p.tile_ends[lo_s - 1] : 0;
+    const int first = lo_s > 0 ? ends[lo_s - 1] : 0;
     int lo, n, ctx;
     bool bad;
-    prefill_seq(p, lo_s, &lo, &n, &ctx, &bad);
+    if (near_seqs) {
+      lo = s_seq[lo_s].x;
+      n = s_seq[lo_s].y;
+      ctx = s_seq[lo_s].z;
+    } else {
+      prefill_seq(p, lo_s, &lo, &n, &ctx, &bad);
+    }
     const int per = p.rows / p.group;           // tokens of a tile
     const int t0 = (i - first) * per;
     PrefillEntry e;
@@ -177,7 +195,7 @@ __global__ void __launch_bounds__(kPrefillPlanThreads) prefill_plan_kernel(const
   for (int i = tid; i < tiles; i += kPrefillPlanThreads) {
     const PrefillEntry e = tile_entry(i);
     if (i == tid) mine = e;
-    p.tile_steps[i] = e.step1;
+    steps[i] = e.step1;
     longest = max(longest, e.step1);
   }
   for (int o = 16; o > 0; o >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
@@ -190,16 +208,16 @@ __global__ void __launch_bounds__(kPrefillPlanThreads) prefill_plan_kernel(const
   {
     const int units = max(1, tiles * p.num_kv_heads);
     const int cut = warp < 16 ? warp + 1 : max(1, (warp - 15) * p.ctas / units);
-    const int limit = p.max_slots > 0 ? max(min(top, kMinSplitSteps), (top + cut - 1) / cut) : max(top, 1);
+    const int limit = p.max_slots > 0 ? max(min(top, p.cost.min_steps), (top + cut - 1) / cut) : max(top, 1);
     const float big = 0.5f * min(top, limit);
     float work = 0.f, big_work = 0.f;
     int bigs = 0, slots = 0, merges = 0;
     for (int i = lane; i < tiles; i += 32) {
-      const int n = p.tile_steps[i];
+      const int n = steps[i];
       const int k = pieces_of(n, max(limit, 1));
-      const float each = (k > 1 ? static_cast<float>((n + k - 1) / k) + kPartialSteps : static_cast<float>(n)) + kPieceSteps;
+      const float each = (k > 1 ? static_cast<float>((n + k - 1) / k) + p.cost.partial : static_cast<float>(n)) + p.cost.piece;
       work += k * each;
-      if (each > big + kPieceSteps) {
+      if (each > big + p.cost.piece) {
         bigs += k;
         big_work += k * each;
       }
@@ -219,7 +237,7 @@ __global__ void __launch_bounds__(kPrefillPlanThreads) prefill_plan_kernel(const
       const float h = static_cast<float>(p.num_kv_heads), c = static_cast<float>(p.ctas);
       float est = work * h / c;
       if (bigs > 0) est = fmaxf(est, ceilf(bigs * h / c) * (big_work / bigs));
-      if (merges > 0) est += kMergeSteps;
+      if (merges > 0) est += p.cost.merge;
       const bool fits = slots <= p.max_slots && merges <= p.max_merges;
       s_est[warp] = fits || warp == 0 ? est : INFINITY;
       s_limit[warp] = max(limit, 1);
@@ -237,7 +255,7 @@ __global__ void __launch_bounds__(kPrefillPlanThreads) prefill_plan_kernel(const
   };
   for (int pass = 0; pass < 2; ++pass) {
     for (int i = tid; i < tiles; i += kPrefillPlanThreads) {
-      const int n = i == tid ? mine.step1 : p.tile_steps[i];
+      const int n = i == tid ? mine.step1 : steps[i];
       const int k = pieces_of(n, limit);
       const int len = (n + k - 1) / k;
       const int bucket = bucket_of(len);

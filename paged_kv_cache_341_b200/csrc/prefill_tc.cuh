@@ -127,7 +127,11 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wi
 }
 
 constexpr int kChunkThreads = 320;
-constexpr int kChunkStages = 5;                  // K/V tiles in flight
+// K/V tiles in flight: as many as fit with head_dim 128 (32 KB each); with 64 more
+// than 6 gain nothing (8,192 tokens on 16,384: 1.49 ms with 6, 1.51 with 5, 1.57
+// with 11)
+template <int D>
+constexpr int kChunkStages = D == 128 ? 5 : 6;
 #ifndef PA_CHUNK_POLY_EXP
 #define PA_CHUNK_POLY_EXP 4
 #endif
@@ -138,7 +142,7 @@ constexpr int kChunkGroupBars = 6;
 template <int D>
 __host__ __device__ constexpr size_t prefill_umma_smem_bytes() {
   const size_t n = 1024 + 2 * static_cast<size_t>(D / 64) * 128 * 128            // Q tiles
-                   + kChunkStages * static_cast<size_t>(D / 64) * 128 * 128      // K/V ring
+                   + kChunkStages<D> * static_cast<size_t>(D / 64) * 128 * 128      // K/V ring
                    + 1024 + 512;                                                 // (m, l) of a row, barriers
   return n < kUmmaMinSmem ? kUmmaMinSmem : n;
 }
@@ -173,7 +177,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   constexpr uint32_t kTileBytes = 16 * kAtomRow;         // 128 tokens
   constexpr uint32_t kQPanel = 128 * 128;
   constexpr uint32_t kQBytes = kHalves * kQPanel;
-  constexpr int NS = kChunkStages;
+  constexpr int NS = kChunkStages<D>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   using M = MmaType<T>;
 
@@ -265,20 +269,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (steps == 0) continue;
       const bool dual = chunk_dual(en, G, steps);
       const int ahead = dual ? 2 : 1;
-      // Q, once the last S of the unit before has completed
-      if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (loaded & 1) ^ 1, abort_flag))) {
-        ok = false;
-        break;
-      }
-      if (lane == 0) {
-        const int copies = dual || n1 > 0 ? 2 : 1;
-        mbar_arrive_expect_tx(q_full, copies * kQBytes);
-        for (int g = 0; g < copies; ++g)
-          for (int hf = 0; hf < kHalves; ++hf)
-            tma_load_4d(s_q + g * kQBytes + hf * kQPanel, &tm_q, q_full, 0, hf, h * G, en.tok0 + (dual ? 0 : g * (128 / G)));
-      }
-      __syncwarp();
-      ++loaded;
       const int32_t* table = prm.block_tables + static_cast<int64_t>(en.seq) * prm.max_blocks;
       // first cache row / 8 of this lane's piece of step t
       auto piece_row = [&](int t) {
@@ -334,6 +324,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       auto rows_at = [&](int i) { return i < steps ? piece_row(en.step0 + i) : 0; };
       int ra = rows_at(0), rb = rows_at(1), rc = rows_at(2);
       ok = load(false, en.step0, ra) && (!dual || load(false, en.step0 + 1, rb));
+      if (!ok) break;
+      // Q, once the last S of the unit before has completed (the first K tiles are
+      // on their way by then)
+      if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (loaded & 1) ^ 1, abort_flag))) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        const int copies = dual || n1 > 0 ? 2 : 1;
+        mbar_arrive_expect_tx(q_full, copies * kQBytes);
+        for (int g = 0; g < copies; ++g)
+          for (int hf = 0; hf < kHalves; ++hf)
+            tma_load_4d(s_q + g * kQBytes + hf * kQPanel, &tm_q, q_full, 0, hf, h * G, en.tok0 + (dual ? 0 : g * (128 / G)));
+      }
+      __syncwarp();
+      ++loaded;
       for (int i = 0; ok && i < steps; ++i) {
         const int rv = ra, rk = dual ? rc : rb;
         ra = rb;
@@ -507,7 +513,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const uint32_t t_lane = tmem + g * kUmmaGroupCols + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t s_col = t_lane + kSCol, o_col = t_lane + kOCol;
     const bool negative = prm.qk_scale < 0.f;
-    const float qk = fabsf(prm.qk_scale);
+    // (never zero, so that a masked -inf stays one: the least float32 times any
+    // finite score is no more than 2^-21, whose exponential is 1 to float32)
+    const float qk = fmaxf(fabsf(prm.qk_scale), 1.4e-45f);
     const bool wide = (reinterpret_cast<uintptr_t>(prm.out) & 31) == 0;
     int tiles = 0, done = 0, duals = 0;
     bool ok = true;
@@ -547,12 +555,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         const int nv = lim - t * kStepTokens;              // tokens of this step the row sees
         const bool masked = lim_first < (t + 1) * kStepTokens;       // uniform over the tile
-        float mul = qk;
         if (masked) {
-          mul = 1.f;                                       // scaled here: 0 * inf must not reach the weights
 #pragma unroll
-          for (int j = 0; j < 128; ++j)
-            x[j] = j < nv ? __float_as_uint(__uint_as_float(x[j]) * qk) : 0xff800000u;
+          for (int j = 0; j < 128; ++j) x[j] = j < nv ? x[j] : 0xff800000u;
         }
         float cm[4];
 #pragma unroll
@@ -562,7 +567,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           for (int j = 8; j < 128; j += 8)
             cm[k] = fmax3(cm[k], __uint_as_float(x[j + k]), __uint_as_float(x[j + 4 + k]));
         }
-        const float c = fmaxf(fmax3(cm[0], cm[1], cm[2]), cm[3]) * mul;
+        const float c = fmaxf(fmax3(cm[0], cm[1], cm[2]), cm[3]) * qk;
         if (__any_sync(0xffffffffu, c > m + kTau)) {
           const float mn = c > m + kTau ? c : m;
           const float f = mn != m ? exp2_approx(m - mn) : 1.f;     // 0 when m was -inf
@@ -582,7 +587,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           m = mn;
         }
         const float mu = m == -INFINITY ? 0.f : m;         // nothing visible yet: every weight is 2^-inf
-        const float2 nm2 = make_float2(-mu, -mu), mul2 = make_float2(mul, mul);
+        const float2 nm2 = make_float2(-mu, -mu), qk2 = make_float2(qk, qk);
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int q32 = 0; q32 < 4; ++q32) {
@@ -590,7 +595,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           for (int i = 0; i < 16; ++i) {
             const int j = q32 * 32 + 2 * i;
             float2 e = nm2;
-            ffma2(e, make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), mul2);
+            ffma2(e, make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), qk2);
             x[j] = __float_as_uint(e.x);
             x[j + 1] = __float_as_uint(e.y);
           }

@@ -187,8 +187,8 @@ def test_prefill_rejects_bad_arguments_on_host(pa):
 def test_prefill_workspace_size(pa):
     size = pa.pa_prefill_workspace_size
     assert size(0, 1, 8, 8, 64, 4, 16) == 0 and size(4, 1, 6, 4, 64, 4, 16) == 0
-    # contexts of up to two steps of 128 tokens are never split: the work list only
-    assert size(100, 2, 8, 2, 128, 16, 16) < 4096
+    # contexts of one step of 128 tokens are never split: the work list only
+    assert size(100, 2, 8, 2, 128, 8, 16) < 8192
     # the partials are bounded by the SM count, whatever the context
     a, b = size(16, 1, 64, 8, 128, 1 << 12, 32), size(16, 1, 64, 8, 128, 1 << 16, 32)
     assert a <= b < 200 << 20

@@ -174,6 +174,28 @@ def test_many_sequences(pa):
     case.check(case.call(pa, 0.125, True), 0.125, True)
 
 
+def test_more_tiles_than_planner_threads(pa):
+    case = Case("f16", [100] * 400, [100 + 7 * (i % 5) for i in range(400)], 8, 1, 64, 16, seed=15).device()
+    case.check(case.call(pa, 0.125, True), 0.125, True)
+
+
+def test_calls_on_two_streams_at_once(pa):
+    """Each with its own workspace, in flight together, over and over."""
+    cases = [Case("bf16", [300, 7], [900, 3000], 8, 2, 128, 16, seed=16).device(),
+             Case("f16", [40, 1, 1], [2500, 800, 64], 4, 4, 64, 16, seed=17).device()]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    ws = [pa.prefill_workspace(c.dq.shape[0], len(c.q_lens), c.hq, c.hkv, c.d, c.tables.shape[1], c.bs) for c in cases]
+    outs = [torch.full_like(c.dq, 77.0) for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, o, w, st in zip(cases, outs, ws, streams):
+            c.call(pa, 0.1, True, out=o, workspace=w, stream=st)
+    torch.cuda.synchronize()
+    for c, o in zip(cases, outs):
+        c.check(o, 0.1, True)
+    assert pa.pa_device_error() == 0
+
+
 def test_infinite_keys_in_masked_places(pa):
     """Later tokens' keys may be anything; their weight is zero."""
     case = Case("bf16", [64], [200], 4, 1, 128, 16, seed=6)
