@@ -10,11 +10,12 @@
 // (prefill_plan.cuh): 256 query rows of one KV head as two tiles of 128, and a
 // range of context steps.  Every K/V tile serves both query tiles.
 //
-// Roles (320 threads, so that each may hold 200 registers):
+// Roles (320 threads):
 //   warps 0-7   softmax, four warps per query tile, one thread per row (=
 //               tensor-memory lane): the whole row of 128 scores is read into
-//               registers once, so that the row maximum needs no exchange;
-//               P is rounded to the cache's type and written over S.
+//               registers, so that the row maximum needs no exchange; P is
+//               rounded to the cache's type and written over S.  (Sixteen warps,
+//               four threads per row, were no faster: 1.45 against 1.31 ms.)
 //   warp 8      TMA producer: Q tiles, then K and V tiles alternately through
 //               one ring.  A piece of a cache block (8, 16, ... 128 tokens) is
 //               one box of a 5-D view of the cache that puts the D/64 column
@@ -38,12 +39,23 @@
 //
 // The reference maximum of a row moves only when a score passes it by 2^kTau
 // (then the thread rescales its row of O), which the final division undoes
-// exactly; weights stay below 2^kTau, far from overflow.  S, O and the
-// statistics are float32; P is rounded to the cache's type for the second
+// exactly; weights stay below 2^kTau, far from overflow.  Since it rarely moves,
+// a step's first weights are worked out with the maximum as it stands while the
+// step's own maximum is still being found (exponentials and comparisons use
+// different pipes), and done again where it does: 1.32 -> 1.21 ms.  S, O and
+// the statistics are float32; P is rounded to the cache's type for the second
 // product (its sum is taken before the rounding, whose errors are unbiased).
-// Of every 16 exponentials kChunkPolyExp go to the FMA pipe as a polynomial
-// (relative error 7.5e-5, below half a unit of P in either type): MUFU alone
-// would take as long as both products.
+//
+// Measured: 8,192 tokens on a 16,384-token context (32/8 heads of 128, bf16,
+// blocks of 16) 1.21 ms = 1,367 TFLOP/s, 0.83 of the measured bf16 burst peak;
+// 0.85 of the sustained peak in a loop that runs into the power limit.  What
+// bounds it there is the chain S -> softmax -> PV -> next S of a query tile
+// (about 3,000 cycles for the two tiles' 2,048 of products): exponentials 1,100
+// to 1,300, reading S and the maximum 200, and 200 to 300 for each hand-over
+// between the softmax warps and the tensor core.  Sharing one S buffer between
+// the tiles and giving P its own columns, so that S(t+1) does not wait for P(t),
+// measured no faster, nor did exponentials as polynomials on the FMA pipe (2 or
+// 4 of 16: 1.28 and 1.32 ms) or 208 registers per softmax thread (1.54 ms).
 //
 // Masks are compared only in steps that hold a masked token for some row of
 // the tile; such tokens get weight zero whatever K holds.  V rows behind the
@@ -132,11 +144,6 @@ constexpr int kChunkThreads = 320;
 // with 11)
 template <int D>
 constexpr int kChunkStages = D == 128 ? 5 : 6;
-#ifndef PA_CHUNK_POLY_EXP
-#define PA_CHUNK_POLY_EXP 4
-#endif
-constexpr int kChunkPolyExp = PA_CHUNK_POLY_EXP;
-static_assert(kChunkPolyExp % 2 == 0 && kChunkPolyExp >= 0 && kChunkPolyExp <= 16, "pairs of exponentials");
 constexpr int kChunkGroupBars = 6;
 
 template <int D>
@@ -511,12 +518,32 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;                   // tensor-memory lane = row of the tile
     const uint32_t t_lane = tmem + g * kUmmaGroupCols + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t s_col = t_lane + kSCol, o_col = t_lane + kOCol;
+    const uint32_t s_col = t_lane + kSCol, p_col = s_col, o_col = t_lane + kOCol;
     const bool negative = prm.qk_scale < 0.f;
     // (never zero, so that a masked -inf stays one: the least float32 times any
     // finite score is no more than 2^-21, whose exponential is 1 to float32)
     const float qk = fmaxf(fabsf(prm.qk_scale), 1.4e-45f);
     const bool wide = (reinterpret_cast<uintptr_t>(prm.out) & 31) == 0;
+    const float2 qk2 = make_float2(qk, qk);
+    // the row's 128 scores (of -q for a negative scale)
+    auto read_scores = [&](uint32_t(&x)[128]) {
+      tc::tmem_ld32_at<0>(s_col, x);
+      tc::tmem_ld32_at<32>(s_col + 32, x);
+      tc::tmem_ld32_at<64>(s_col + 64, x);
+      tc::tmem_ld32_at<96>(s_col + 96, x);
+      tc::tmem_wait_ld();
+      if (negative) {
+#pragma unroll
+        for (int j = 0; j < 128; ++j) x[j] ^= 0x80000000u;
+      }
+    };
+    // the P written so far may be read by the tensor core
+    auto hand_over = [&](uint64_t* bar) {
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
     int tiles = 0, done = 0, duals = 0;
     bool ok = true;
     for (int r = 0; ok && r < rounds; ++r) {
@@ -543,35 +570,84 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           break;
         }
         tc::fence_after_sync();
-        uint32_t x[128];
-        tc::tmem_ld32_at<0>(s_col, x);
-        tc::tmem_ld32_at<32>(s_col + 32, x);
-        tc::tmem_ld32_at<64>(s_col + 64, x);
-        tc::tmem_ld32_at<96>(s_col + 96, x);
-        tc::tmem_wait_ld();
-        if (negative) {
+        const bool masked = lim_first < (t + 1) * kStepTokens;          // uniform over the tile
+        bool moved = masked || t == begin;                 // the reference maximum may have to move
+        if (!moved) {
+          // Nothing masked: the weights of the first half are worked out with the
+          // maximum as it stands while the step's own maximum is found beside them
+          // (different pipes); only if that passes the threshold is this undone.
+          uint32_t x[128];
+          read_scores(x);
+          const float2 nm2 = make_float2(-m, -m);
+          float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          float cm[4];
 #pragma unroll
-          for (int j = 0; j < 128; ++j) x[j] ^= 0x80000000u;
+          for (int k = 0; k < 4; ++k) cm[k] = fmaxf(__uint_as_float(x[64 + k]), __uint_as_float(x[68 + k]));
+          // 32 scores from j0 into 16 packed weights; with `top`, their maximum and
+          // that of the 32 scores 64 further on is taken along
+          auto weights = [&](auto tag, int j0, uint32_t(&w)[16]) {
+            constexpr bool kTop = decltype(tag)::value;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int j = j0 + 2 * i;
+              if constexpr (kTop) {
+                cm[i & 3] = fmax3(cm[i & 3], __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+                cm[(i + 2) & 3] = fmax3(cm[(i + 2) & 3], __uint_as_float(x[j + 64]), __uint_as_float(x[j + 65]));
+              }
+              float2 v = nm2;
+              ffma2(v, make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), qk2);
+              v.x = exp2_approx(v.x);
+              v.y = exp2_approx(v.y);
+              w[i] = M::pack(v.x, v.y);
+              fadd2(ls[i & 1], v);
+            }
+          };
+          uint32_t w0[16], w1[16];
+          weights(std::true_type{}, 0, w0);
+          weights(std::true_type{}, 32, w1);
+          const float c = fmaxf(fmax3(cm[0], cm[1], cm[2]), cm[3]) * qk;
+          moved = __any_sync(0xffffffffu, !(c <= m + kTau && m > -INFINITY));
+          if (!moved) {
+            tc::tmem_st16(p_col, w0);
+            tc::tmem_st16(p_col + 16, w1);
+            hand_over(p_half(g));
+            weights(std::false_type{}, 64, w0);
+            tc::tmem_st16(p_col + 32, w0);
+            weights(std::false_type{}, 96, w1);
+            tc::tmem_st16(p_col + 48, w1);
+            hand_over(p_full(g));
+            fadd2(l2, ls[0]);
+            fadd2(l2, ls[1]);
+          }
         }
-        const int nv = lim - t * kStepTokens;              // tokens of this step the row sees
-        const bool masked = lim_first < (t + 1) * kStepTokens;       // uniform over the tile
-        if (masked) {
+        if (moved) {
+          // The first steps of a row, and steps with masked tokens: 32 scores at a
+          // time, read twice (P over S stays behind the scores still to be read).
+          const int nv = lim - t * kStepTokens;            // tokens of this step the row sees
+          auto scores = [&](int q, uint32_t(&x)[32]) {
+            tc::tmem_ld32(s_col + 32 * q, x);
+            tc::tmem_wait_ld();
+            if (negative) {
 #pragma unroll
-          for (int j = 0; j < 128; ++j) x[j] = j < nv ? x[j] : 0xff800000u;
-        }
-        float cm[4];
+              for (int j = 0; j < 32; ++j) x[j] ^= 0x80000000u;
+            }
+            if (masked) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          cm[k] = fmaxf(__uint_as_float(x[k]), __uint_as_float(x[4 + k]));
+              for (int j = 0; j < 32; ++j) x[j] = j < nv - 32 * q ? x[j] : 0xff800000u;
+            }
+          };
+          float ext = -INFINITY;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t x[32];
+            scores(q, x);
 #pragma unroll
-          for (int j = 8; j < 128; j += 8)
-            cm[k] = fmax3(cm[k], __uint_as_float(x[j + k]), __uint_as_float(x[j + 4 + k]));
-        }
-        const float c = fmaxf(fmax3(cm[0], cm[1], cm[2]), cm[3]) * qk;
-        if (__any_sync(0xffffffffu, c > m + kTau)) {
+            for (int j = 0; j < 32; j += 2) ext = fmax3(ext, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+          }
+          const float c = ext * qk;
           const float mn = c > m + kTau ? c : m;
           const float f = mn != m ? exp2_approx(m - mn) : 1.f;     // 0 when m was -inf
-          if (t > begin) {
+          if (t > begin && __any_sync(0xffffffffu, mn != m)) {
 #pragma unroll 1
             for (int ob = 0; ob < D / 16; ++ob) {
               uint32_t o[16];
@@ -585,57 +661,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           l2.x *= f;
           l2.y *= f;
           m = mn;
-        }
-        const float mu = m == -INFINITY ? 0.f : m;         // nothing visible yet: every weight is 2^-inf
-        const float2 nm2 = make_float2(-mu, -mu), qk2 = make_float2(qk, qk);
-        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float mu = m == -INFINITY ? 0.f : m;       // nothing visible yet: every weight is 2^-inf
+          const float2 nm2 = make_float2(-mu, -mu);
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t x[32], w[16];
+            scores(q, x);
 #pragma unroll
-        for (int q32 = 0; q32 < 4; ++q32) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int j = q32 * 32 + 2 * i;
-            float2 e = nm2;
-            ffma2(e, make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), qk2);
-            x[j] = __float_as_uint(e.x);
-            x[j + 1] = __float_as_uint(e.y);
-          }
-          if (masked) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              x[q32 * 32 + j] = __float_as_uint(exp2_approx(__uint_as_float(x[q32 * 32 + j])));
-          } else {
-#pragma unroll
-            for (int b = 0; b < 32; b += 16) {
-#pragma unroll
-              for (int j = 0; j < 16 - kChunkPolyExp; ++j)
-                x[q32 * 32 + b + j] = __float_as_uint(exp2_approx(__uint_as_float(x[q32 * 32 + b + j])));
-#pragma unroll
-              for (int j = 16 - kChunkPolyExp; j < 16; j += 2) {
-                const int k = q32 * 32 + b + j;
-                const float2 y = exp2_poly2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
-                x[k] = __float_as_uint(y.x);
-                x[k + 1] = __float_as_uint(y.y);
-              }
+            for (int i = 0; i < 16; ++i) {
+              float2 v = nm2;
+              ffma2(v, make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), qk2);
+              v.x = exp2_approx(v.x);                      // (exact zeros for masked scores)
+              v.y = exp2_approx(v.y);
+              w[i] = M::pack(v.x, v.y);
+              fadd2(l2, v);
             }
-          }
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int j = q32 * 32 + 2 * i;
-            const float2 y = make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
-            w[i] = M::pack(y.x, y.y);
-            fadd2(ls[i & 1], y);
-          }
-          tc::tmem_st16(s_col + q32 * 16, w);
-          if (q32 == 1 || q32 == 3) {
-            tc::tmem_wait_st();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q32 == 1 ? p_half(g) : p_full(g));
+            tc::tmem_st16(p_col + 16 * q, w);
+            if (q & 1) hand_over(q == 1 ? p_half(g) : p_full(g));
           }
         }
-        fadd2(l2, ls[0]);
-        fadd2(l2, ls[1]);
       }
       if (!ok) break;
       float l = l2.x + l2.y;

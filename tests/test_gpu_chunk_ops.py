@@ -253,8 +253,8 @@ def test_cross_attention_over_a_cache_of_encoder_states(pa):
     cache.attend_chunks(q.cuda(), starts, out, 0.125, causal=False)
     kh, vh = cache.k_cache.double().cpu().numpy(), cache.v_cache.double().cpu().numpy()
     ref = oracle_prefill(q.double().numpy(), kh, vh, cache.tables, lens, starts.cpu().numpy(), 0.125, causal=False)
-    # roundings of weights and output (2^-11 each, |out| <= max |V|), polynomial exponentials 1.5e-4
-    assert np.abs(out.double().cpu().numpy() - ref).max() <= (2 * 2 ** -11 + 2e-4) * np.abs(v.double().numpy()).max()
+    # roundings of weights and output (2^-11 each, |out| <= max |V|), and 2 ctx 2^-23 of the float32 sums
+    assert np.abs(out.double().cpu().numpy() - ref).max() <= (2 * 2 ** -11 + 300 * 2 ** -23) * np.abs(v.double().numpy()).max()
     assert (out[25:] == 0).all()
 
 
