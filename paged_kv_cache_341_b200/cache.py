@@ -242,6 +242,28 @@ class PagedKVCache:
         kinds = {4: torch.int32, 8: torch.int64}
         return [dev[o:o + a.nbytes].view(kinds[a.dtype.itemsize]).view(a.shape) for a, o in zip(arrays, offsets)]
 
+    def _check_rotary(self, q, k_new, v_new, total, inv_freq, positions, pair_axis, q_out):
+        """Refusals of ``pa_rope_append`` that ``prefill_step`` makes before it changes the host tables."""
+        for t in (q, k_new, v_new):
+            if total and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != self.head_dim)
+                          or t.stride(0) * t.element_size() % 16 or t.data_ptr() % 16):
+                raise ValueError("q, k_new and v_new must have contiguous, 16-byte aligned token rows")
+        ints = [(positions, "positions"), (pair_axis, "pair_axis")]
+        for t, name, dtype in [(inv_freq, "inv_freq", torch.float32)] + [(t, n, torch.int32) for t, n in ints]:
+            if t is not None and not (t.is_cuda and t.dtype == dtype and t.is_contiguous()
+                                      and t.get_device() == q.get_device()):
+                raise TypeError("%s must be a contiguous %s tensor on q's device" % (name, dtype))
+        if not 0 < 2 * inv_freq.numel() <= self.head_dim:
+            raise ValueError("inv_freq must have between 1 and head_dim / 2 entries")
+        if positions is not None and (positions.dim() not in (1, 2) or positions.shape[-1] != total
+                                      or positions.numel() == 0 and total):
+            raise ValueError("positions must be [axes, T] or [T]")
+        if pair_axis is not None and pair_axis.numel() != inv_freq.numel():
+            raise ValueError("pair_axis must have one entry per pair of inv_freq")
+        if q_out is not None and not (q_out.is_cuda and q_out.dtype == self.dtype and q_out.shape == q.shape
+                                      and q_out.is_contiguous() and q_out.get_device() == q.get_device()):
+            raise ValueError("q_out must be a contiguous tensor like q")
+
     def prefill_step(self, q, k_new, v_new, out, scale, counts, rows=None, inv_freq=None, positions=None,
                      pair_axis=None, interleaved=False, q_out=None, workspace=None, stream=None):
         """A chunk of ``counts[i]`` new tokens for each of ``rows`` (a ``slice``, default all): reserve, copy-on-write,
@@ -271,8 +293,19 @@ class PagedKVCache:
         for t in (q, k_new, v_new, out):
             if not t.is_cuda or t.dtype != self.dtype:
                 raise TypeError("q, k_new, v_new and out must be CUDA tensors of the cache's dtype")
+            if t.get_device() != torch.cuda.current_device():
+                raise ValueError("q, k_new, v_new and out must be on the current device")
         if q.shape[1] % self.num_kv_heads or q.shape[1] // self.num_kv_heads not in (1, 2, 4, 8):
             raise ValueError("query heads per KV head must be 1, 2, 4 or 8")
+        if self.head_dim not in (64, 128) or (self.block_size != 8 and self.block_size % 16):
+            raise ValueError("chunk steps need head_dim 64 or 128, and blocks of 8 or a multiple of 16 tokens")
+        if not out.is_contiguous():
+            raise ValueError("out must be contiguous")
+        if inv_freq is None:
+            if not (q.is_contiguous() and k_new.is_contiguous() and v_new.is_contiguous()):
+                raise ValueError("q, k_new and v_new must be contiguous")
+        else:
+            self._check_rotary(q, k_new, v_new, total, inv_freq, positions, pair_axis, q_out)
         before = lens.copy()
         slots, pairs, updates = self.pool.pa_reserve_chunks(tables, lens, counts, r0)
         starts = np.zeros(counts.size + 1, np.int32)
@@ -310,6 +343,14 @@ class PagedKVCache:
         moves (int32 [M, 2] of old and new id).
         """
         stream = stream or torch.cuda.current_stream()
+        for c in [c for pair in layers for c in pair]:          # refused before the host tables change
+            if not c.is_cuda or c.shape != self.k_cache.shape or c.dtype != self.dtype or not c.is_contiguous():
+                raise ValueError("every layer's caches must be like this cache's")
+        if len({c.data_ptr() for pair in layers for c in pair} | {self.k_cache.data_ptr(), self.v_cache.data_ptr()}) \
+                != 2 * len(layers) + 2:
+            raise ValueError("the caches must be distinct")
+        if self.k_cache.get_device() != torch.cuda.current_device():
+            raise ValueError("the cache must be on the current device")
         moves = self.pool.pa_pool_compact(self.tables)
         if len(moves):
             d_moves, = self._send([moves], stream)

@@ -424,15 +424,17 @@ def pa_move_blocks(k_caches, v_caches, moves, block_tables=None, stream=None):
     if n == 0 or len(v_caches) != n:
         raise ValueError("need as many K caches as V caches, at least one")
     shape, dt = k_caches[0].shape, k_caches[0].dtype
-    if len({c.data_ptr() for caches in (k_caches, v_caches) for c in caches}) != 2 * n:
+    ptrs = [c.data_ptr() for caches in (k_caches, v_caches) for c in caches]
+    if len(set(ptrs)) != 2 * n:
         raise ValueError("the caches must be distinct")
     dev = torch.cuda.current_device() if k_caches[0].is_cuda else -2
-    kp, vp = (_vp * n)(), (_vp * n)()
-    for caches, ptrs in ((k_caches, kp), (v_caches, vp)):
-        for i, c in enumerate(caches):
+    for caches in (k_caches, v_caches):
+        for c in caches:
             if c.shape != shape:
                 raise ValueError("all caches must have the shape of the first")
-            ptrs[i] = _ptr(c, "cache", dt, dev)
+            if c.dtype is not dt or c.get_device() != dev or not c.is_contiguous():
+                _refuse(c, "cache", dt, dev)
+    kp, vp = (_vp * n)(*ptrs[:n]), (_vp * n)(*ptrs[n:])
     rows = cols = stride = 0
     tp = None
     if block_tables is not None and block_tables.numel():

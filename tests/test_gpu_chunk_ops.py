@@ -157,6 +157,30 @@ def test_moves_report_bad_ids_and_order(pa):
     assert pa.pa_device_error() == 0
 
 
+def test_compaction_of_a_cache_with_several_layers(pa):
+    """`PagedKVCache.compact` moves further layers that share its pool and tables."""
+    from paged_kv_cache_341_b200.cache import PagedKVCache
+    rng = np.random.default_rng(3)
+    cache = PagedKVCache(30, 16, 2, 64, torch.float16, 3, 8, initial_free_order=rng.permutation(30), fill=0.0)
+    layers = [tuple(workloads.randn((30, 16, 2, 64), "f16", 10 * i + j).cuda() for j in range(2)) for i in range(3)]
+    for r in range(3):
+        cache.allocate(r, 40 + 30 * r)
+    cache.upload_tables()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    ids = [torch.from_numpy(cache.tables[r, :-(-int(cache.lens[r]) // 16)].astype(np.int64)) for r in range(3)]
+    before = [[[c[i.cuda()].cpu() for i in ids] for c in pair] for pair in layers]
+    moves = cache.compact(layers=layers, stream=side)
+    side.synchronize()
+    assert len(moves) and np.array_equal(cache.d_tables.cpu().numpy(), cache.tables)
+    for pair, old in zip(layers, before):
+        for c, rows in zip(pair, old):
+            for r in range(3):
+                now = torch.from_numpy(cache.tables[r, :len(ids[r])].astype(np.int64))
+                assert torch.equal(c[now.cuda()].cpu(), rows[r])
+    assert len(cache.compact(layers=layers)) == 0
+
+
 def _rows(cache, row):
     n = int(cache.lens[row])
     ids = cache.tables[row, :-(-n // cache.block_size)]
@@ -270,6 +294,23 @@ def test_prefill_step_refuses_before_it_reserves(pa):
             cache.prefill_step(*args, 0.1, counts)
     with pytest.raises(TypeError):
         cache.prefill_step(q.float(), k, k, q, 0.1, [4, 1])
+    freq = torch.ones(32, device="cuda")
+    for kw in (dict(inv_freq=freq, positions=torch.zeros(4, dtype=torch.int32, device="cuda")),
+               dict(inv_freq=torch.ones(33, device="cuda")),
+               dict(inv_freq=freq, pair_axis=torch.zeros(31, dtype=torch.int32, device="cuda")),
+               dict(inv_freq=freq, q_out=q[:4]), dict(inv_freq=freq, q_out=q.float())):
+        with pytest.raises(ValueError):
+            cache.prefill_step(q, k, k, q.clone(), 0.1, [4, 1], **kw)
+    for kw in (dict(inv_freq=freq.double()), dict(inv_freq=freq, positions=torch.zeros(5, device="cuda"))):
+        with pytest.raises(TypeError):
+            cache.prefill_step(q, k, k, q.clone(), 0.1, [4, 1], **kw)
+    wide = torch.zeros((5, 8, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):                                # strided rows need the rotary append
+        cache.prefill_step(wide[:, :4], k, k, q.clone(), 0.1, [4, 1])
+    with pytest.raises(ValueError):
+        cache.compact(layers=[(cache.k_cache, cache.v_cache.clone())])
+    with pytest.raises(ValueError):
+        cache.compact(layers=[(cache.k_cache[:2], cache.v_cache.clone())])
     with pytest.raises(pa.PoolExhausted):
         big = torch.zeros((70, 4, 64), dtype=torch.bfloat16, device="cuda")
         kv = torch.zeros((70, 2, 64), dtype=torch.bfloat16, device="cuda")
