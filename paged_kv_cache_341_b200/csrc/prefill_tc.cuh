@@ -57,6 +57,12 @@
 // measured no faster, nor did exponentials as polynomials on the FMA pipe (2 or
 // 4 of 16: 1.28 and 1.32 ms) or 208 registers per softmax thread (1.54 ms).
 //
+// Between units a query tile waits for the other tile's last products and for
+// its Q (about 8,000 cycles from one unit's last score to the next one's first).
+// Issuing the next unit's first S with this one's last products measured no
+// faster: the longer issue loop lost what the shorter gap gained (1.23 against
+// 1.19 ms; prompts of 1,300 units 237 against 221 us).
+//
 // Masks are compared only in steps that hold a masked token for some row of
 // the tile; such tokens get weight zero whatever K holds.  V rows behind the
 // context's end are zeroed in shared memory (a weight of zero would not undo
@@ -282,7 +288,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int tok = t * kStepTokens + lane * piece_rows;
         if (lane >= pieces || tok >= en.ctx) return 0;
         const int b = tok / BS;
-        int phys = __ldg(table + b);
+        int phys = table[b];                     // (not through the read-only path: it may be newer than this grid)
         if (phys < 0 || phys >= prm.num_blocks) {
           set_device_error(DEVERR_BAD_BLOCK_ID);
           phys = 0;
