@@ -317,3 +317,40 @@ def test_prefill_step_refuses_before_it_reserves(pa):
         cache.prefill_step(big, kv, kv, big.clone(), 0.1, [35, 35])
     assert cache.lens.sum() == 0 and cache.pool.pa_pool_num_free() == 4 and (cache.tables == -1).all()
     assert math.isfinite(float(q.sum()))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_offsets_beyond_32_bits(pa, dtype):
+    """The last blocks of a cache of more than 2^31 elements: attention, append and moves give the bits that they
+    give in a small cache."""
+    hq, hkv, d, bs, nb = 8, 8, 128, 16, 140000
+    t, ctx = 20, 300
+    n = -(-ctx // bs)
+    dt = TORCH[dtype]
+    big = [torch.empty((nb, bs, hkv, d), dtype=dt, device="cuda") for _ in range(2)]
+    assert big[0].numel() > 2 ** 31
+    small = [workloads.randn((n + 2, bs, hkv, d), dtype, i).cuda() for i in range(2)]
+    high = nb - 1 - torch.arange(n + 2)                           # block i of the small cache is block high[i]
+    for b, s in zip(big, small):
+        b[high.cuda()] = s
+    q, k, v = (workloads.randn((t, h, d), dtype, 10 + i).cuda() for i, h in enumerate((hq, hkv, hkv)))
+    pos = torch.arange(ctx - t, ctx, dtype=torch.int32, device="cuda")
+    freq = torch.ones(64, device="cuda") / torch.arange(1, 65, device="cuda")
+    starts = torch.tensor([0, t], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([ctx], dtype=torch.int32, device="cuda")
+    results = []
+    for caches, ids in ((small, torch.arange(n + 2)), (big, high)):
+        token = torch.arange(ctx - t, ctx)
+        slots = (ids[token // bs].long() * bs + token % bs).cuda()
+        q_out, out = torch.empty_like(q), torch.empty_like(q)
+        table = ids[:n].to(torch.int32)[None].cuda()
+        pa.pa_rope_append(q, k, v, pos, freq, slots, *caches, q_out)
+        pa.pa_prefill_attention(q_out, *caches, table, lens, starts, 0.09, out)
+        pair = sorted([int(ids[0]), int(ids[n])])                 # one block on to an unused one
+        moves = torch.tensor([pair], dtype=torch.int32, device="cuda")
+        pa.pa_move_blocks([caches[0]], [caches[1]], moves)
+        assert pa.pa_device_error() == 0
+        assert torch.equal(caches[0][pair[0]], caches[0][pair[1]])
+        results.append((out, q_out, caches[0].view(-1, hkv, d)[slots], caches[1].view(-1, hkv, d)[slots]))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
