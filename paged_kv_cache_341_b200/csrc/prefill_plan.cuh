@@ -106,6 +106,7 @@ __global__ void __launch_bounds__(kPrefillPlanThreads) prefill_plan_kernel(const
   s_hist[tid] = 0;
   static_assert(kPrefillBuckets == kPrefillPlanThreads, "one bucket per thread");
   wait_prerequisite_grids();
+  __syncthreads();                              // every warp sees the zeroes (the wait orders no warps)
 
   // inclusive scan of one int per thread over the CTA; *total = the sum
   auto scan = [&](int v, int* total) {
