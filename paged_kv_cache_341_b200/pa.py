@@ -418,7 +418,8 @@ def pa_move_blocks(k_caches, v_caches, moves, block_tables=None, stream=None):
     """Run a compaction's moves on every layer's cache and rewrite the device block tables.
 
     k_caches/v_caches: sequences of [NB, bs, Hkv, D] CUDA tensors, one per layer; moves: int32 CUDA [M, 2] of
-    (source, destination), sources increasing; block_tables: int32 CUDA [rows, cols] with unit column stride.
+    (source, destination), sources increasing; block_tables: int32 CUDA [rows, cols] with unit column stride and rows
+    that do not overlap.
     """
     n = len(k_caches)
     if n == 0 or len(v_caches) != n:
@@ -427,6 +428,14 @@ def pa_move_blocks(k_caches, v_caches, moves, block_tables=None, stream=None):
     ptrs = [c.data_ptr() for caches in (k_caches, v_caches) for c in caches]
     if len(set(ptrs)) != 2 * n:
         raise ValueError("the caches must be distinct")
+    rows = cols = stride = 0
+    if block_tables is not None and block_tables.numel():
+        if block_tables.dim() != 2 or block_tables.stride(1) != 1:
+            raise ValueError("block_tables must be a 2-D tensor with unit column stride")
+        rows, cols = block_tables.shape
+        stride = block_tables.stride(0) if rows > 1 else cols
+        if stride < cols:
+            raise ValueError("the rows of block_tables must not overlap")
     dev = torch.cuda.current_device() if k_caches[0].is_cuda else -2
     for caches in (k_caches, v_caches):
         for c in caches:
@@ -435,15 +444,10 @@ def pa_move_blocks(k_caches, v_caches, moves, block_tables=None, stream=None):
             if c.dtype is not dt or c.get_device() != dev or not c.is_contiguous():
                 _refuse(c, "cache", dt, dev)
     kp, vp = (_vp * n)(*ptrs[:n]), (_vp * n)(*ptrs[n:])
-    rows = cols = stride = 0
     tp = None
-    if block_tables is not None and block_tables.numel():
-        if block_tables.dim() != 2 or block_tables.stride(1) != 1:
-            raise ValueError("block_tables must be a 2-D tensor with unit column stride")
+    if rows:
         if block_tables.dtype is not torch.int32 or block_tables.get_device() != dev:
             _refuse(block_tables, "block_tables", torch.int32, dev)
-        rows, cols = block_tables.shape
-        stride = max(block_tables.stride(0), cols)
         tp = block_tables.data_ptr()
     nb, bs, hkv, d = shape
     _check(_lib.pa_move_blocks(kp, vp, n, _ptr(moves, "moves", torch.int32, dev), moves.numel() // 2, nb, bs, hkv, d,
