@@ -322,8 +322,8 @@ size_t pa_prefill_workspace_size(int32_t num_tokens, int32_t num_seqs, int32_t n
  * weight of zero.  Lengths or starts out of range are clamped and set device
  * error 2; block ids outside the pool set device error 1.
  * Supported: head_dim 64 or 128; Hq/Hkv in {1,2,4,8}; block_size a multiple of
- * 16, or 8; f32/f16/bf16.  Errors: PA_ERR_INVALID, PA_ERR_UNSUPPORTED,
- * PA_ERR_CUDA. */
+ * 16, or 8; f32/f16/bf16; scale * log2(e) finite in float32.  Errors:
+ * PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_CUDA. */
 pa_status pa_prefill_attention(const void* q, const void* k_cache, const void* v_cache, int32_t num_blocks,
                                const int32_t* block_tables, int32_t max_blocks_per_seq,
                                const int32_t* context_lens, const int32_t* q_starts, int32_t num_tokens,

@@ -124,7 +124,7 @@ pa_status launch_prefill(const PrefillArgs& a) {
   prm.block_size = a.BS;
   prm.num_blocks = a.num_blocks;
   prm.causal = a.causal;
-  prm.qk_scale = a.scale * 1.4426950408889634f;
+  prm.qk_scale = a.scale * pa::kLog2e;
 
   // every kernel is a programmatic dependent of the one before it: it is set up
   // early, and reads nothing before its wait

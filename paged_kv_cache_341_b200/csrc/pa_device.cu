@@ -5,6 +5,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 #include <cstdlib>
 #include <mutex>
@@ -812,8 +813,9 @@ pa_status pa_prefill_attention(const void* q, const void* k_cache, const void* v
     return pa::fail(PA_ERR_INVALID, "pa_prefill_attention: pool or table too large for 32-bit token indices");
   if (static_cast<long long>(num_tokens) * num_q_heads >= (1ll << 31))
     return pa::fail(PA_ERR_INVALID, "pa_prefill_attention: too many query rows for 32-bit indices");
-  if (!(scale == scale) || scale > 3.0e38f || scale < -3.0e38f)
-    return pa::fail(PA_ERR_INVALID, "pa_prefill_attention: scale must be finite");
+  // (the kernels work in units of log2: a product that is not finite would make a zero score a NaN)
+  if (!std::isfinite(scale * pa::kLog2e))
+    return pa::fail(PA_ERR_INVALID, "pa_prefill_attention: scale * log2(e) must be finite");
   if (num_tokens == 0 || num_seqs == 0) return pa::ok();
   if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !q_starts || !out)
     return pa::fail(PA_ERR_INVALID, "pa_prefill_attention: null pointer");

@@ -27,6 +27,8 @@
 
 namespace pa {
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 struct PrefillParams {
   const void* q;                 // [T][Hq][D]
   const void* k_cache;           // [num_blocks][block_size][Hkv][D]
