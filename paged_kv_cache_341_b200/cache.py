@@ -23,6 +23,9 @@ the copy pairs, plus whatever the caller passes from host memory.  The whole
 tables go over once, with ``upload_tables``.
 """
 
+import ctypes
+import math
+
 import numpy as np
 import torch
 
@@ -215,27 +218,44 @@ class PagedKVCache:
                                 self.d_lens if lens is None else lens, q_starts, scale, out, causal=causal,
                                 workspace=workspace, stream=stream)
 
-    def _send(self, arrays, stream):
-        """Copy int32/int64 numpy arrays to the device in one transfer; returns their device views.
+    def _here(self, stream):
+        """``stream`` or the current one; refuses what is not a stream, and any device but the current one."""
+        device = torch.cuda.current_device()
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        elif not isinstance(stream, torch.cuda.Stream):
+            raise TypeError("stream must be a torch.cuda.Stream")
+        if self.k_cache.get_device() != device or stream.device_index != device:
+            raise ValueError("the cache and the stream must be on the current device")
+        return stream
+
+    def _stage(self, sizes, stream):
+        """Buffers for one transfer of arrays of up to ``sizes`` bytes each; nothing is sent.
 
         The pinned side is double-buffered and grows on demand; the device side is a fresh buffer of ``stream``.
         """
+        total = sum(-(-int(n) // 8) * 8 for n in sizes)
+        b = self._chunk & 1
+        if self._chunk_done[b] is not None:
+            self._chunk_done[b].synchronize()             # the transfer out of this host buffer has finished
+        if self._chunk_host[b] is None or self._chunk_host[b].numel() < total:
+            self._chunk_host[b] = torch.empty(max(4096, 2 * total), dtype=torch.uint8).pin_memory()
+        with torch.cuda.stream(stream):
+            return torch.empty(max(total, 8), dtype=torch.uint8, device=self.device)
+
+    def _send(self, arrays, dev, stream):
+        """Copy int32/int64 numpy arrays to ``dev`` (of ``_stage``) in one transfer; returns their device views."""
         offsets, total = [], 0
         for a in arrays:
             offsets.append(total)
             total += -(-a.nbytes // 8) * 8
         b = self._chunk & 1
         self._chunk += 1
-        if self._chunk_done[b] is not None:
-            self._chunk_done[b].synchronize()             # the transfer out of this host buffer has finished
-        if self._chunk_host[b] is None or self._chunk_host[b].numel() < total:
-            self._chunk_host[b] = torch.empty(max(4096, 2 * total), dtype=torch.uint8).pin_memory()
         host = self._chunk_host[b]
         raw = host.numpy()
         for a, o in zip(arrays, offsets):
             raw[o:o + a.nbytes] = np.ascontiguousarray(a).reshape(-1).view(np.uint8)
         with torch.cuda.stream(stream):
-            dev = torch.empty(max(total, 8), dtype=torch.uint8, device=self.device)
             dev[:total].copy_(host[:total], non_blocking=True)
             self._chunk_done[b] = torch.cuda.Event()
             self._chunk_done[b].record(stream)
@@ -245,8 +265,9 @@ class PagedKVCache:
     def _check_rotary(self, q, k_new, v_new, total, inv_freq, positions, pair_axis, q_out):
         """Refusals of ``pa_rope_append`` that ``prefill_step`` makes before it changes the host tables."""
         for t in (q, k_new, v_new):
-            if total and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != self.head_dim)
-                          or t.stride(0) * t.element_size() % 16 or t.data_ptr() % 16):
+            row = t.shape[1] * self.head_dim
+            if total and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != self.head_dim) or total > 1
+                          and (t.stride(0) < row or t.stride(0) * t.element_size() % 16)):
                 raise ValueError("q, k_new and v_new must have contiguous, 16-byte aligned token rows")
         ints = [(positions, "positions"), (pair_axis, "pair_axis")]
         for t, name, dtype in [(inv_freq, "inv_freq", torch.float32)] + [(t, n, torch.int32) for t, n in ints]:
@@ -263,6 +284,25 @@ class PagedKVCache:
         if q_out is not None and not (q_out.is_cuda and q_out.dtype == self.dtype and q_out.shape == q.shape
                                       and q_out.is_contiguous() and q_out.get_device() == q.get_device()):
             raise ValueError("q_out must be a contiguous tensor like q")
+        if q_out is not None and (q_out.data_ptr() % 16 or q_out.data_ptr() == q.data_ptr()
+                                  and not q.is_contiguous()):
+            raise ValueError("q_out must be 16-byte aligned, and may be q only when q is contiguous")
+
+    def _check_attention(self, total, num_seqs, num_q_heads, scale, workspace):
+        """Refusals of ``pa_prefill_attention`` that ``prefill_step`` makes before it changes the host tables."""
+        if not math.isfinite(ctypes.c_float(ctypes.c_float(scale).value * pa.LOG2E).value):
+            raise ValueError("scale * log2(e) must be finite")
+        if max(self.num_blocks * self.block_size, total * num_q_heads) >= 1 << 31 \
+                or self.max_blocks * self.block_size >= (1 << 31) - 128:
+            raise ValueError("pool, table or chunk too large for 32-bit indices")
+        if workspace is not None and total:
+            if not workspace.is_cuda or workspace.get_device() != torch.cuda.current_device():
+                raise ValueError("workspace must be on the current device")
+            need = pa.pa_prefill_workspace_size(total, num_seqs, num_q_heads, self.num_kv_heads, self.head_dim,
+                                                self.max_blocks, self.block_size)
+            if (not workspace.is_contiguous() or workspace.data_ptr() % 32
+                    or workspace.numel() * workspace.element_size() < need):
+                raise ValueError("workspace must be contiguous, 32-byte aligned and hold %d bytes" % need)
 
     def prefill_step(self, q, k_new, v_new, out, scale, counts, rows=None, inv_freq=None, positions=None,
                      pair_axis=None, interleaved=False, q_out=None, workspace=None, stream=None):
@@ -276,14 +316,14 @@ class PagedKVCache:
         sequence; the turned queries go to ``q_out`` (allocated when not given).  Returns the host slots and copy
         pairs.  A row with count 0 takes no part.
         """
-        stream = stream or torch.cuda.current_stream()
+        # everything that can be refused is refused, and everything allocated, before the host tables change
+        stream = self._here(stream)
         sel = slice(None) if rows is None else rows
         r0 = sel.start or 0
         tables, lens = self.tables[sel], self.lens[sel]
         assert tables.flags.c_contiguous and lens.flags.c_contiguous
         counts = np.ascontiguousarray(np.asarray(counts, np.int32))
         total = int(counts.sum(dtype=np.int64))
-        # everything that can be refused is refused before the host tables change
         if counts.size != lens.size or (counts.size and int(counts.min()) < 0):
             raise ValueError("counts must have one entry >= 0 per row")
         kv_shape = (total, self.num_kv_heads, self.head_dim)
@@ -301,36 +341,42 @@ class PagedKVCache:
             raise ValueError("chunk steps need head_dim 64 or 128, and blocks of 8 or a multiple of 16 tokens")
         if not out.is_contiguous():
             raise ValueError("out must be contiguous")
+        if any(t.data_ptr() % 16 for t in (q, k_new, v_new, out)):
+            raise ValueError("q, k_new, v_new and out must be 16-byte aligned")
+        self._check_attention(total, counts.size, q.shape[1], scale, workspace)
         if inv_freq is None:
             if not (q.is_contiguous() and k_new.is_contiguous() and v_new.is_contiguous()):
                 raise ValueError("q, k_new and v_new must be contiguous")
         else:
             self._check_rotary(q, k_new, v_new, total, inv_freq, positions, pair_axis, q_out)
+        own_positions = inv_freq is not None and positions is None
+        most_updates = int((-(-counts.astype(np.int64) // self.block_size)).sum()) + counts.size + 1
+        dev = self._stage([8 * total, self.lens.nbytes, 4 * counts.size + 4, 12 * most_updates, 8 * counts.size,
+                           4 * total if own_positions else 0], stream)
+        with torch.cuda.stream(stream):
+            if inv_freq is not None and q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            if workspace is None and total:
+                workspace = pa.prefill_workspace(total, counts.size, q.shape[1], self.num_kv_heads, self.head_dim,
+                                                 self.max_blocks, self.block_size, device=self.device)
         before = lens.copy()
         slots, pairs, updates = self.pool.pa_reserve_chunks(tables, lens, counts, r0)
         starts = np.zeros(counts.size + 1, np.int32)
         np.cumsum(counts, out=starts[1:])
         arrays = [slots, self.lens, starts, updates, pairs]
-        if inv_freq is not None and positions is None:
+        if own_positions:
             arrays.append((np.arange(total) + np.repeat(before - starts[:-1], counts)).astype(np.int32))
-        sent = self._send(arrays, stream)
+        sent = self._send(arrays, dev, stream)
         d_slots, d_lens, d_starts, d_upd, d_pairs = sent[:5]
         pa.pa_update_block_tables(self.d_tables, d_upd, self.d_lens, d_lens, stream=stream)
         self.copy_blocks(d_pairs, stream=stream)
         if inv_freq is not None:
-            if q_out is None:
-                with torch.cuda.stream(stream):
-                    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
             pa.pa_rope_append(q, k_new, v_new, sent[5] if positions is None else positions, inv_freq, d_slots,
                               self.k_cache, self.v_cache, q_out, pair_axis=pair_axis, interleaved=interleaved,
                               stream=stream)
             q = q_out
         else:
             self.append(k_new, v_new, d_slots, stream=stream)
-        if workspace is None and total:
-            with torch.cuda.stream(stream):
-                workspace = pa.prefill_workspace(total, counts.size, q.shape[1], self.num_kv_heads, self.head_dim,
-                                                 self.max_blocks, self.block_size, device=self.device)
         self.attend_chunks(q, d_starts, out, scale, tables=self.d_tables[sel], lens=self.d_lens[sel],
                            workspace=workspace, stream=stream)
         return slots, pairs
@@ -353,7 +399,7 @@ class PagedKVCache:
             raise ValueError("the cache must be on the current device")
         moves = self.pool.pa_pool_compact(self.tables)
         if len(moves):
-            d_moves, = self._send([moves], stream)
+            d_moves, = self._send([moves], self._stage([moves.nbytes], stream), stream)
             pa.pa_move_blocks([self.k_cache] + [k for k, _ in layers], [self.v_cache] + [v for _, v in layers],
                               d_moves, self.d_tables, stream=stream)
         return moves

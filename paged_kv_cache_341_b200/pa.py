@@ -23,6 +23,7 @@ _lib = ctypes.CDLL(_LIB_PATH)
 
 PA_OK, PA_ERR_EXHAUSTED, PA_ERR_INVALID, PA_ERR_REFCOUNT, PA_ERR_CUDA, PA_ERR_DEVICE_CHECK, PA_ERR_UNSUPPORTED = range(7)
 PA_F32, PA_F16, PA_BF16 = 0, 1, 2
+LOG2E = ctypes.c_float(1.4426950408889634).value      # as the kernels hold it, in 32 bits
 DTYPE_CODE = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16}
 
 # Every symbol include/pa.h declares, with its C signature.
