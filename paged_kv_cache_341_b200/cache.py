@@ -388,20 +388,30 @@ class PagedKVCache:
         in the same launch.  Block tables change on both sides (the device ones must be up to date).  Returns the
         moves (int32 [M, 2] of old and new id).
         """
-        stream = stream or torch.cuda.current_stream()
-        for c in [c for pair in layers for c in pair]:          # refused before the host tables change
+        # everything that can be refused is refused, and everything allocated, before the host tables change
+        stream = self._here(stream)
+        layers = [(self.k_cache, self.v_cache)] + [tuple(pair) for pair in layers]
+        if any(len(pair) != 2 for pair in layers):
+            raise ValueError("layers must be (k_cache, v_cache) pairs")
+        for c in [c for pair in layers for c in pair]:
             if not c.is_cuda or c.shape != self.k_cache.shape or c.dtype != self.dtype or not c.is_contiguous():
                 raise ValueError("every layer's caches must be like this cache's")
-        if len({c.data_ptr() for pair in layers for c in pair} | {self.k_cache.data_ptr(), self.v_cache.data_ptr()}) \
-                != 2 * len(layers) + 2:
+            if c.get_device() != torch.cuda.current_device() or c.data_ptr() % 16:
+                raise ValueError("every layer's caches must be on the current device, 16-byte aligned")
+        if len({c.data_ptr() for pair in layers for c in pair}) != 2 * len(layers):
             raise ValueError("the caches must be distinct")
-        if self.k_cache.get_device() != torch.cuda.current_device():
-            raise ValueError("the cache must be on the current device")
+        block_bytes = self.block_size * self.num_kv_heads * self.head_dim * self.k_cache.element_size()
+        if block_bytes % 16:
+            raise ValueError("blocks must be a multiple of 16 bytes")
+        # (no more moves than free or live blocks; a launch has a CTA per move, cache of up to 64 layers and 16 KB)
+        free = self.pool.pa_pool_num_free()
+        if 2 * min(len(layers), 64) * min(free, self.num_blocks - free) * -(-block_bytes // 16384) >= 1 << 30:
+            raise ValueError("too many moves for one launch")
+        dev = self._stage([8 * (self.num_blocks // 2 + 1)], stream)
         moves = self.pool.pa_pool_compact(self.tables)
         if len(moves):
-            d_moves, = self._send([moves], self._stage([moves.nbytes], stream), stream)
-            pa.pa_move_blocks([self.k_cache] + [k for k, _ in layers], [self.v_cache] + [v for _, v in layers],
-                              d_moves, self.d_tables, stream=stream)
+            d_moves, = self._send([moves], dev, stream)
+            pa.pa_move_blocks([k for k, _ in layers], [v for _, v in layers], d_moves, self.d_tables, stream=stream)
         return moves
 
     def engine(self, num_q_heads, partition_size=0, stream=None):

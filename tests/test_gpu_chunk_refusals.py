@@ -136,3 +136,39 @@ def test_one_row_of_any_stride_and_steps_of_no_tokens(pa):
     want = torch.empty_like(out)
     other.prefill_step(q[:1], k[:1], v[:1], want, 0.1, [0, 1, 0], inv_freq=freq)
     assert torch.equal(out, want) and same(state(cache), state(other))
+
+
+def test_refused_compactions_leave_the_state_as_it_was(pa):
+    cache, q, k, v, freq = filled()
+    cache.release(0)
+    cache.release(2)                                              # (row 0's sharer: now there is a block to move)
+    cache.upload_tables()
+    before = state(cache)
+    shape = cache.k_cache
+    other = [torch.randn_like(shape), torch.randn_like(shape)]
+    bad = [dict(layers=[(shifted(other[0]), other[1])]), dict(layers=[(other[0], shifted(other[1]))]),
+           dict(layers=[(other[0].cpu(), other[1].cpu())]), dict(layers=[(other[0], other[1], other[1])]),
+           dict(layers=[(other[0],)]), dict(layers=[(other[0], other[0])]), dict(layers=[(shape, other[1])]),
+           dict(layers=[(other[0].float(), other[1].float())]), dict(stream=7)]
+    for kw in bad:
+        with pytest.raises((ValueError, TypeError, pa.PagedAttnError)):
+            cache.compact(**kw)
+        assert same(state(cache), before), str(kw)
+    old = [c.clone() for c in other]
+    moves = cache.compact(layers=iter([tuple(other)]))            # (any iterable of pairs)
+    assert len(moves)
+    for now, was in zip(other, old):
+        assert torch.equal(now[moves[:, 1].tolist()], was[moves[:, 0].tolist()])
+    assert np.array_equal(cache.d_tables.cpu().numpy(), cache.tables)
+    assert pa.pa_device_error() == 0
+
+
+def test_compaction_of_blocks_that_fill_no_16_bytes_is_refused(pa):
+    from paged_kv_cache_341_b200.cache import PagedKVCache
+    cache = PagedKVCache(6, 1, 1, 2, torch.float32, 2, 4, initial_free_order=[5, 4, 3, 2, 1, 0], fill=0.0)
+    cache.allocate(0, 2)
+    cache.upload_tables()
+    before = state(cache)
+    with pytest.raises((ValueError, pa.PagedAttnError)):
+        cache.compact()
+    assert same(state(cache), before)
