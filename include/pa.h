@@ -168,7 +168,13 @@ pa_status pa_seq_alloc_prompt(pa_pool* pool, const int32_t* tokens, int32_t num_
  * goes to pairs_out ([S][2] room); updates_out (or NULL) receives the table
  * entries written, (row0 + s, column, block id), room for the sum over s of
  * ceil(counts[s] / block_size) + 1 triples.  All or nothing.  Errors as for
- * pa_seq_reserve_slot, and PA_ERR_INVALID for a negative count. */
+ * pa_seq_reserve_slot, and PA_ERR_INVALID for a negative count.
+ * A row that pa_seq_alloc_prompt filled holds the blocks of its whole prompt:
+ * its tokens go to their slots in the table (block * block_size + offset), and
+ * its length is num_tokens before anything is reserved behind it.  In a pool
+ * with prefix caching a chunk that would take new blocks in the place of live
+ * ones behind the row's length is therefore refused (PA_ERR_INVALID): set the
+ * entries of a released row to -1. */
 pa_status pa_reserve_chunks(pa_pool* pool, int32_t* tables, int32_t table_cap, int32_t* lens,
                             const int32_t* counts, int32_t num_seqs, int32_t row0, int64_t* slots_out,
                             int32_t* pairs_out, int32_t* num_pairs_out, int32_t* updates_out,

@@ -315,6 +315,10 @@ class PagedKVCache:
         (``pa_rope_append``): ``positions`` int32 [axes, T] on the device, by default each token's place in its
         sequence; the turned queries go to ``q_out`` (allocated when not given).  Returns the host slots and copy
         pairs.  A row with count 0 takes no part.
+
+        A row that holds its prompt's blocks already (``pa_seq_alloc_prompt``) is refused until its length is the
+        prompt's: its tokens go to their slots in the row's table (``append``, ``pa_rope_append``), and
+        ``attend_chunks`` reads them.
         """
         # everything that can be refused is refused, and everything allocated, before the host tables change
         stream = self._here(stream)

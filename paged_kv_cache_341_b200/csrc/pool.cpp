@@ -257,6 +257,15 @@ pa_status pa_reserve_chunks(pa_pool* pool, int32_t* tables, int32_t table_cap, i
   for (int32_t s = 0; s < num_seqs; ++s) {
     if (counts[s] < 0) return pa::fail(PA_ERR_INVALID, "pa_reserve_chunks: negative count");
     total += counts[s];
+    // A prompt's blocks are in its row already (pa_seq_alloc_prompt).  New ones in
+    // their place would lose them, and leave content keys of blocks never written.
+    if (!pool->prefix_cache || lens[s] < 0) continue;
+    const int32_t* table = tables + static_cast<int64_t>(s) * table_cap;
+    const int64_t bs = pool->block_size, end = static_cast<int64_t>(lens[s]) + counts[s];
+    for (int64_t c = (lens[s] + bs - 1) / bs; c < table_cap && c * bs < end; ++c)
+      if (pool->valid_id(table[c]) && pool->refcount[table[c]] > 0)
+        return pa::fail(PA_ERR_INVALID, "pa_reserve_chunks: sequence " + std::to_string(s) +
+                                            " holds blocks behind its length (pa_seq_alloc_prompt)");
   }
   // only tokens that take a block or a copy change anything but the length:
   // those are undone one by one, the lengths at once
