@@ -450,9 +450,12 @@ def pa_move_blocks(k_caches, v_caches, moves, block_tables=None, stream=None):
         if block_tables.dtype is not torch.int32 or block_tables.get_device() != dev:
             _refuse(block_tables, "block_tables", torch.int32, dev)
         tp = block_tables.data_ptr()
+    mp = _ptr(moves, "moves", torch.int32, dev)
+    if moves.dim() != 2 or moves.shape[1] != 2:
+        raise ValueError("moves must be [M, 2]")
     nb, bs, hkv, d = shape
-    _check(_lib.pa_move_blocks(kp, vp, n, _ptr(moves, "moves", torch.int32, dev), moves.numel() // 2, nb, bs, hkv, d,
-                               tp, rows, cols, stride, DTYPE_CODE[dt], _raw_stream(stream, dev)))
+    _check(_lib.pa_move_blocks(kp, vp, n, mp, moves.shape[0], nb, bs, hkv, d, tp, rows, cols, stride,
+                               DTYPE_CODE[dt], _raw_stream(stream, dev)))
 
 
 def pa_prefill_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,

@@ -172,3 +172,15 @@ def test_compaction_of_blocks_that_fill_no_16_bytes_is_refused(pa):
     with pytest.raises((ValueError, pa.PagedAttnError)):
         cache.compact()
     assert same(state(cache), before)
+
+
+@pytest.mark.parametrize("shape", [(2, 3), (4,), (3,), (2, 2, 1), (1, 4)])
+def test_move_lists_that_are_not_pairs_are_refused(pa, shape):
+    """A list laid out as all sources, then all destinations, would be taken for other pairs."""
+    k, v = (workloads.randn((8, 8, 1, 64), "f32", i).cuda() for i in (1, 2))
+    old = k.clone(), v.clone()
+    moves = torch.arange(int(np.prod(shape)), dtype=torch.int32, device="cuda").reshape(shape)
+    with pytest.raises(ValueError):
+        pa.pa_move_blocks([k], [v], moves)
+    torch.cuda.synchronize()
+    assert torch.equal(k, old[0]) and torch.equal(v, old[1])
