@@ -308,11 +308,14 @@ size_t pa_prefill_workspace_size(int32_t num_tokens, int32_t num_seqs, int32_t n
  *   lim = context_lens[s]               causal == 0: every token sees the
  *                                       whole context (cross attention to an
  *                                       encoder's states kept in the cache).
- * A row with lim <= 0 is zero.  K_s, V_s as for pa_decode_attention; a chunk of
- * one token with causal != 0 is that call's row.  Scores, softmax statistics
- * and output are accumulated in float32; for f16 and bf16 caches the weights
- * are rounded to that type for the product with V.  Results do not depend on
- * scheduling: equal calls give equal bits.
+ * A row with lim <= 0 is zero.  A visible score of -infinity has weight zero (a
+ * row of nothing else is zero); one that is NaN or +infinity makes its row NaN.
+ * K_s, V_s as for pa_decode_attention; a chunk of one token with causal != 0 is
+ * that call's row.
+ * Scores, softmax statistics and output are accumulated in float32; for f16 and
+ * bf16 caches the weights are rounded to that type for the product with V (off by
+ * 2^-11 and 2^-8 of a weight at most).  Results do not depend on scheduling: equal
+ * calls give equal bits.
  *
  *   q, out        device [T][Hq][D]; rows of out from q_starts[S] on (and
  *                 before q_starts[0]) are not written

@@ -318,7 +318,8 @@ class PagedKVCache:
 
         A row that holds its prompt's blocks already (``pa_seq_alloc_prompt``) is refused until its length is the
         prompt's: its tokens go to their slots in the row's table (``append``, ``pa_rope_append``), and
-        ``attend_chunks`` reads them.
+        ``attend_chunks`` reads them.  ``decode_step`` and the engine append keys as they are given: the tokens that
+        follow a prompt with rotary positions come as chunks of one, or turned by the caller.
         """
         # everything that can be refused is refused, and everything allocated, before the host tables change
         stream = self._here(stream)

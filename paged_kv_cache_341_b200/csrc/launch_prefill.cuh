@@ -36,7 +36,8 @@ struct PrefillArgs {
 };
 
 // The plan is made for at most this many CTAs, so that the workspace size is a
-// function of the arguments alone (a B200 has 148 SMs).
+// function of the arguments alone (a B200 has 148 SMs); the grid of the 16-bit
+// kernel, one CTA per SM, is bounded by it too.
 constexpr int kPrefillMaxCtas = 148;
 
 // Workspace: [header 256 B][tile ends][tile steps][entries][merges][partial (m, l)][partial outputs].
@@ -117,7 +118,6 @@ pa_status launch_prefill(const PrefillArgs& a) {
   prm.part_ml = reinterpret_cast<float2*>(ws + L.ml);
   prm.part_acc = reinterpret_cast<float*>(ws + L.acc);
   prm.out = a.out;
-  prm.num_tokens = a.T;
   prm.num_kv_heads = a.Hkv;
   prm.group = a.Hq / a.Hkv;
   prm.max_blocks = a.max_blocks;

@@ -14,7 +14,11 @@
 // registers.  Bound by the FMA pipe and the shared-memory reads that feed it.
 // Small tiles, several CTAs per SM: tiles of 64 rows x 64 tokens with 256
 // threads took 10 us each for a handful of rows (4 sequences of up to 45 tokens
-// on 300, head_dim 64: 43 us for the kernel, 13 in this form).
+// on 300, head_dim 64: 43 us for the kernel, 13 in this form).  With many rows
+// the six shared-memory reads for 32 products of a thread set the pace: 512 tokens
+// on a 4,096-token context, 32/8 heads, take 1.52 ms (head_dim 128) and 0.80 ms
+// (64), 21 and 20 TFLOP/s, 0.28 of the 74 TFLOP/s that 148 SMs multiply and add
+// at 1.965 GHz.
 #ifndef PAGEDATTN_PREFILL_CUH
 #define PAGEDATTN_PREFILL_CUH
 
@@ -39,7 +43,7 @@ struct PrefillParams {
   float* part_acc;               // [slot][Hkv][rows][D]
   float2* part_ml;               // [slot][Hkv][rows], m in units of log2
   void* out;                     // [T][Hq][D]
-  int num_tokens, num_kv_heads, group;
+  int num_kv_heads, group;
   int max_blocks, block_size, num_blocks;
   int causal;
   float qk_scale;                // scale * log2(e)

@@ -54,7 +54,7 @@ struct PlanCost {
   int min_steps;                 // a piece of a split context is at least about this long
   float piece, partial, merge;   // in steps, as above
 };
-// (a step takes about 1.5 us with tensor cores, and 4 to 8 us without)
+// (a step takes about 1.5 us with tensor cores, and 4 to 8 us without, of a CTA that has its SM to itself)
 constexpr PlanCost kPlanCost16{2, 2.f, 1.5f, 3.f};
 constexpr PlanCost kPlanCost32{1, 0.5f, 0.2f, 0.7f};
 
@@ -67,7 +67,8 @@ struct PrefillPlanParams {
   PrefillMerge* merges;
   int num_seqs, num_tokens, num_kv_heads, group, rows;
   int causal, cap;               // cap: tokens a table row can hold
-  int ctas;                      // CTAs of the attention grid
+  int ctas;                      // what the estimate spreads the pieces over: one per SM (the float32 kernel
+                                 // runs several CTAs on an SM, which then share its rate)
   int max_tiles, max_merges, max_slots;        // capacities; slots are per KV head
   int* tile_steps;               // [max_tiles]
   PlanCost cost;
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(kPrefillMergeWarps * 32) prefill_merge_kernel(
     for (int k0 = 0; k0 < m.pieces; k0 += 32) {
       const int n = min(32, m.pieces - k0);
       if (m.pieces > 32) ml = lane < n ? p.part_ml[at0 + static_cast<int64_t>(k0 + lane) * per] : make_float2(0.f, 0.f);
-      // (a piece in which nothing is visible has l = 0, and no output was written)
+      // (a piece in which nothing is visible has l = 0: its weight is zero, whatever its row holds)
       const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - top);
       l += f * ml.y;
 #pragma unroll 8

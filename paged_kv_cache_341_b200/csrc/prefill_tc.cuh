@@ -46,10 +46,12 @@
 // the statistics are float32; P is rounded to the cache's type for the second
 // product (its sum is taken before the rounding, whose errors are unbiased).
 //
-// Measured: 8,192 tokens on a 16,384-token context (32/8 heads of 128, bf16,
-// blocks of 16) 1.21 ms = 1,367 TFLOP/s, 0.83 of the measured bf16 burst peak;
-// 0.85 of the sustained peak in a loop that runs into the power limit.  What
-// bounds it there is the chain S -> softmax -> PV -> next S of a query tile
+// Measured, in short bursts as all times in this file: 8,192 tokens on a
+// 16,384-token context (32/8 heads of 128, bf16, blocks of 16) 1.21 ms = 1,367
+// TFLOP/s, 0.83 of the measured bf16 burst peak.  As a call among others it runs
+// into the power limit: 1.41 ms = 1,170 TFLOP/s, 0.84 of the sustained peak.
+// With head_dim 64 that call takes 1.07 ms = 769 TFLOP/s, its exponentials alone
+// 0.69 ms.  What bounds the burst is the chain S -> softmax -> PV -> next S of a query tile
 // (about 3,000 cycles for the two tiles' 2,048 of products): exponentials 1,100
 // to 1,300, reading S and the maximum 200, and 200 to 300 for each hand-over
 // between the softmax warps and the tensor core.  Sharing one S buffer between
